@@ -39,6 +39,11 @@ _SIGS = {
     "wq_ptq1_1_encode": ([_p, _i64, _i64, _p, _p, _p, _p, _i64, _p], _i),
     "wq_gemv_ternary_ptq1_1": ([_p, _p, _p, _p, _i64, _p, _i64, _i64, _i64, _p, _p], _i),
     "wq_gemv_ternary_ptq1_1_pt": ([_p, _p, _p, _p, _i64, _p, _i64, _i64, _i64, _p, _p], _i),
+    "wq_sort_rows_workspace": ([_i64, _i64, _i64], _i64),
+    "wq_sort_rows": ([_p, _i64, _i64, _i64, _p, _p, _p, _p, _i64, _p], _i),
+    "wq_dispatch_rows": ([_p, _i, _p, _i64, _i64, _i64, _p, _p], _i),
+    "wq_combine_rows": ([_p, _i, _p, _p, _i64, _i64, _i64, _p, _p], _i),
+    "wq_combine_rows_grad": ([_p, _p, _i, _p, _p, _i64, _i64, _i64, _p, _p, _p], _i),
     # calibration kernels (include/wq_peaks.h)
     "wq_peak_read_sink_words": ([], _i64),
     "wq_peak_read": ([_p, _i64, _p, _i64, _p], _i),
@@ -329,6 +334,115 @@ def _gemv_ternary_ptq1_1(name, superblocks, codebook, esc_idx, esc_patt, x_q8, k
                                     _ptr(esc_idx, d) if n_esc else None,
                                     _ptr(esc_patt, d) if n_esc else None, n_esc,
                                     _ptr(x_q8, d), n, k, c, _ptr(out, d), _sptr(st)))
+
+
+# ---- rows that go to different weights: the sort, the moves, the products
+# of the sorted rows
+
+_ROW_DTYPES = (torch.float32, torch.float16, torch.bfloat16)
+
+
+def _call(name, st, *args):
+    """The C function on stream ``st``, with the stream's device current."""
+    fn = getattr(load_library(), name)
+    if st.device_index == torch.cuda.current_device():
+        _check(name, fn(*args, st.cuda_stream))
+    else:
+        with torch.cuda.device(st.device_index):
+            _check(name, fn(*args, st.cuda_stream))
+
+
+def _workspace(name, st, workspace, need):
+    """The caller's workspace (any dtype), or one from torch's allocator that
+    is reused in the order of stream ``st`` alone."""
+    if need < 0:
+        raise WqError(name, need)
+    if workspace is not None:
+        nbytes = workspace.numel() * workspace.element_size()
+        _require(nbytes >= need, f"workspace holds {nbytes} bytes, {need} are needed")
+        return workspace, nbytes
+    if need == 0:
+        return None, 0
+    with torch.cuda.stream(st):
+        return torch.empty(need, dtype=torch.uint8, device=st.device), need
+
+
+def _plan_i32(*tensors):
+    for t in tensors:
+        _require(t.dtype == torch.int32, "ids, offsets, order and place are int32")
+
+
+def wq_sort_rows_workspace(t, topk, bins):
+    """Bytes of workspace that wq_sort_rows needs for these sizes."""
+    need = lib.wq_sort_rows_workspace(t, topk, bins)
+    if need < 0:
+        raise WqError("wq_sort_rows_workspace", need)
+    return need
+
+
+def wq_sort_rows(ids, bins, offsets, order, place, workspace=None, stream=None):
+    """Stable sort of the slots of ids int32 [t][topk] (or [t]) by bin:
+    offsets [bins + 1], order and place [t * topk], all int32.  Ids outside
+    [0, bins) are dropped."""
+    _require(ids.dim() in (1, 2), "ids is [t][topk] or [t]")
+    t, topk = ids.shape[0], ids.shape[1] if ids.dim() == 2 else 1
+    _plan_i32(ids, offsets, order, place)
+    _require(offsets.numel() == bins + 1, "offsets hold bins + 1 values")
+    _require(order.numel() == t * topk and place.numel() == t * topk, "order and place hold t * topk values")
+    st = _stream(stream)
+    d = st.device
+    args = (_ptr(ids, d), t, topk, bins, _ptr(offsets, d), _ptr(order, d), _ptr(place, d))
+    ws, nbytes = _workspace("wq_sort_rows", st, workspace, lib.wq_sort_rows_workspace(t, topk, bins))
+    _call("wq_sort_rows", st, *args, _ptr(ws, d), nbytes)
+
+
+def _moved(x, place, rows):
+    """t, topk, h of x [t][h], place [t][topk] (or [t]) and rows [t * topk][h]."""
+    _require(x.dim() == 2 and rows.dim() == 2, "rows are [rows][h]")
+    _require(place.dim() in (1, 2) and place.shape[0] == x.shape[0], "place is [t][topk]")
+    t, h = x.shape
+    topk = place.shape[1] if place.dim() == 2 else 1
+    _plan_i32(place)
+    _require(rows.dtype == x.dtype, "both sides have one dtype")
+    _require(tuple(rows.shape) == (t * topk, h), "the sorted rows are [t * topk][h]")
+    return t, topk, h
+
+
+def wq_dispatch_rows(x, place, out, stream=None):
+    """out[place[i][j]] = x[i]: x [t][h] (f32, f16 or bf16) to out [t * topk][h]."""
+    t, topk, h = _moved(x, place, out)
+    st = _stream(stream)
+    d = st.device
+    _call("wq_dispatch_rows", st, _ptr(x, d), _dtype(x, _ROW_DTYPES), _ptr(place, d), t, topk, h, _ptr(out, d))
+
+
+def _row_weights(weights, place):
+    _require(weights.dtype == torch.float32 and weights.numel() == place.numel(), "weights are fp32 [t][topk]")
+
+
+def wq_combine_rows(rows, place, weights, out, stream=None):
+    """out[i] = sum_j weights[i][j] * rows[place[i][j]] (weights fp32 [t][topk],
+    or None for 1).  With None also the gradient of wq_dispatch_rows."""
+    t, topk, h = _moved(out, place, rows)
+    if weights is not None:
+        _row_weights(weights, place)
+    st = _stream(stream)
+    d = st.device
+    _call("wq_combine_rows", st, _ptr(rows, d), _dtype(rows, _ROW_DTYPES), _ptr(place, d), _ptr(weights, d), t, topk, h,
+          _ptr(out, d))
+
+
+def wq_combine_rows_grad(d_out, rows, place, weights, d_rows, d_weights, stream=None):
+    """Gradients of wq_combine_rows: d_rows[place[i][j]] = weights[i][j] * d_out[i]
+    and d_weights[i][j] = <d_out[i], rows[place[i][j]]> (fp32)."""
+    t, topk, h = _moved(d_out, place, rows)
+    _moved(d_out, place, d_rows)
+    _row_weights(weights, place)
+    _row_weights(d_weights, place)
+    st = _stream(stream)
+    d = st.device
+    _call("wq_combine_rows_grad", st, _ptr(d_out, d), _ptr(rows, d), _dtype(rows, _ROW_DTYPES), _ptr(place, d),
+          _ptr(weights, d), t, topk, h, _ptr(d_rows, d), _ptr(d_weights, d))
 
 
 # ---- calibration kernels (include/wq_peaks.h): practical ceilings of the

@@ -109,6 +109,14 @@ int gemv_ternary_ptq1_1(const uint8_t* superblocks, const uint8_t* codebook, con
   return hip_status(wq::launch_gemv_ternary_sb(superblocks, codebook, esc_idx, esc_patt, n_esc, x_q8, pt,
                                                n, k, c, out, as_stream(stream)));
 }
+
+bool valid_dtype(int dt) { return dt == WQ_F32 || dt == WQ_F16 || dt == WQ_BF16; }
+
+// sizes shared by the calls that move rows: false if refused
+bool valid_rows(int64_t t, int64_t topk, int64_t h) {
+  return mul_sat(t, topk) <= wq::kMaxSlots && h < (int64_t(1) << 31) &&
+         mul_sat(t, h / 1024 + 1) <= kMaxGrid;  // at least 1024 elements a workgroup, or whole rows
+}
 }  // namespace
 
 extern "C" {
@@ -263,6 +271,64 @@ int wq_gemv_ternary_ptq1_1_pt(const uint8_t* superblocks, const uint8_t* codeboo
                               void* stream) {
   return gemv_ternary_ptq1_1(superblocks, codebook, esc_idx, esc_patt, n_esc, x_pt, true, n, k, c, out,
                              stream);
+}
+
+
+int64_t wq_sort_rows_workspace(int64_t t, int64_t topk, int64_t bins) {
+  if (t < 0 || topk < 0 || bins < 0) return WQ_EINVAL;
+  if (bins < 1 || bins > wq::kMaxBins || mul_sat(t, topk) > wq::kMaxSlots) return WQ_ESHAPE;
+  return (int64_t)wq::sort_rows_workspace(t * topk, bins);
+}
+
+int wq_sort_rows(const int32_t* ids, int64_t t, int64_t topk, int64_t bins, int32_t* offsets, int32_t* order,
+                 int32_t* place, void* workspace, int64_t workspace_bytes, void* stream) {
+  const int64_t need = wq_sort_rows_workspace(t, topk, bins);
+  if (need < 0) return (int)need;
+  const int64_t slots = t * topk;
+  if (!offsets || (slots > 0 && (!ids || !order || !place))) return WQ_EINVAL;
+  if (workspace_bytes < need || (need > 0 && !workspace)) return WQ_EINVAL;
+  if (!aligned(ids, 4) || !aligned(offsets, 4) || !aligned(order, 4) || !aligned(place, 4) ||
+      !aligned(workspace, 4))
+    return WQ_EALIGN;
+  return hip_status(wq::launch_sort_rows(ids, slots, bins, offsets, order, place, workspace, as_stream(stream)));
+}
+
+int wq_dispatch_rows(const void* x, int dtype, const int32_t* place, int64_t t, int64_t topk, int64_t h, void* out,
+                     void* stream) {
+  if (t < 0 || topk < 0 || h < 0 || !valid_dtype(dtype)) return WQ_EINVAL;
+  if (t == 0 || topk == 0 || h == 0) return WQ_OK;
+  if (!x || !place || !out) return WQ_EINVAL;
+  if (!valid_rows(t, topk, h)) return WQ_ESHAPE;
+  const uintptr_t es = (uintptr_t)dtype_size(dtype);
+  if (!aligned(x, es) || !aligned(out, es) || !aligned(place, 4)) return WQ_EALIGN;
+  return hip_status(wq::launch_dispatch_rows(x, dtype, place, t, topk, h, out, as_stream(stream)));
+}
+
+int wq_combine_rows(const void* rows, int dtype, const int32_t* place, const float* weights, int64_t t, int64_t topk,
+                    int64_t h, void* out, void* stream) {
+  if (t < 0 || topk < 0 || h < 0 || !valid_dtype(dtype)) return WQ_EINVAL;
+  if (t == 0 || h == 0) return WQ_OK;
+  if (topk == 0) return WQ_ESHAPE;  // a sum over no slots would have to be written
+  if (!rows || !place || !out) return WQ_EINVAL;
+  if (!valid_rows(t, topk, h)) return WQ_ESHAPE;
+  const uintptr_t es = (uintptr_t)dtype_size(dtype);
+  if (!aligned(rows, es) || !aligned(out, es) || !aligned(place, 4) || !aligned(weights, 4)) return WQ_EALIGN;
+  return hip_status(wq::launch_combine_rows(rows, dtype, place, weights, t, topk, h, out, as_stream(stream)));
+}
+
+int wq_combine_rows_grad(const void* d_out, const void* rows, int dtype, const int32_t* place, const float* weights,
+                         int64_t t, int64_t topk, int64_t h, void* d_rows, float* d_weights, void* stream) {
+  if (t < 0 || topk < 0 || h < 0 || !valid_dtype(dtype)) return WQ_EINVAL;
+  if (t == 0 || topk == 0) return WQ_OK;
+  if (h == 0) return WQ_ESHAPE;  // d_weights would have to be written
+  if (!d_out || !rows || !place || !weights || !d_rows || !d_weights) return WQ_EINVAL;
+  if (!valid_rows(t, topk, h)) return WQ_ESHAPE;
+  const uintptr_t es = (uintptr_t)dtype_size(dtype);
+  if (!aligned(d_out, es) || !aligned(rows, es) || !aligned(d_rows, es) || !aligned(place, 4) ||
+      !aligned(weights, 4) || !aligned(d_weights, 4))
+    return WQ_EALIGN;
+  return hip_status(wq::launch_combine_rows_grad(d_out, rows, dtype, place, weights, t, topk, h, d_rows, d_weights,
+                                                 as_stream(stream)));
 }
 
 }  // extern "C"

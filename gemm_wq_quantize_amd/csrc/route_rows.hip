@@ -1,0 +1,471 @@
+// Rows sorted by bin, and moved there and back (gfx950).
+//
+// A bin is an expert of a mixture layer, or an adapter: whatever picks the
+// weights that a row meets.  The sort is a stable counting sort of the slots
+// s = token * topk + j by their bin; the moves go by the sort's inverse, token
+// by token, so a token's row is read once however many bins it goes to.
+#include "wq_internal.h"
+
+namespace wq {
+namespace {
+
+// ---------------------------------------------------------------- the sort
+//
+// One 512-lane workgroup sorts SORT_CHUNK slots: each of its 8 waves takes 512
+// consecutive slots, 64 at a time.  A wave finds the lanes that share a key
+// with one ballot per key bit, so a slot's rank among them comes from the
+// lane order and the result is stable with no atomic whose order matters; one
+// LDS counter per (wave, bin) carries the count from one 64 to the next.  Two
+// scans (over the waves of a bin, then over the bins) turn the counters into
+// positions.  With more than one chunk a counting launch goes first, and each
+// workgroup sums the counts of the chunks before its own by itself: a third
+// launch for that sum would cost more than these reads from L2 (32 chunks of
+// 257 counters at 131072 slots in 256 bins).
+constexpr int SORT_THREADS = 512, SORT_WAVES = SORT_THREADS / 64, SORT_IT = 8;
+constexpr int SORT_CHUNK = SORT_THREADS * SORT_IT;
+constexpr int SORT_BPT = (kMaxBins + 1 + SORT_THREADS - 1) / SORT_THREADS;  // counters per lane, at most
+
+__device__ __forceinline__ int sort_key(int id, int bins) { return (unsigned)id < (unsigned)bins ? id : bins; }
+
+__global__ __launch_bounds__(SORT_THREADS) void k_sort_count(const int* __restrict__ ids, int slots, int bins,
+                                                             int* __restrict__ counts) {
+  __shared__ int hist[kMaxBins + 1];
+  const int nb = bins + 1;
+  for (int i = threadIdx.x; i < nb; i += SORT_THREADS) hist[i] = 0;
+  __syncthreads();
+#pragma unroll
+  for (int it = 0; it < SORT_IT; ++it) {
+    const int s = (int)blockIdx.x * SORT_CHUNK + it * SORT_THREADS + (int)threadIdx.x;
+    if (s < slots) atomicAdd(&hist[sort_key(ids[s], bins)], 1);
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < nb; i += SORT_THREADS) counts[(int64_t)blockIdx.x * nb + i] = hist[i];
+}
+
+__global__ __launch_bounds__(SORT_THREADS) void k_sort_place(const int* __restrict__ ids, int slots, int bins,
+                                                             int key_bits, const int* __restrict__ counts,
+                                                             int* __restrict__ offsets, int* __restrict__ order,
+                                                             int* __restrict__ place) {
+  __shared__ int hist[SORT_WAVES * (kMaxBins + 1)];
+  __shared__ int wave_sum[SORT_WAVES];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, nb = bins + 1;
+  const int blk = blockIdx.x, nblk = gridDim.x;
+  for (int i = tid; i < SORT_WAVES * nb; i += SORT_THREADS) hist[i] = 0;
+  __syncthreads();
+
+  const int s0 = blk * SORT_CHUNK + wave * (64 * SORT_IT) + lane;
+  int* mine = hist + wave * nb;
+  int tag[SORT_IT];  // key | position among the wave's slots of that key << 11
+#pragma unroll
+  for (int it = 0; it < SORT_IT; ++it) {
+    const int s = s0 + it * 64;
+    const bool live = s < slots;
+    const int key = live ? sort_key(ids[s], bins) : bins;
+    uint64_t same = __ballot(live);
+    if (same == 0) continue;  // wave-uniform: past the last slot
+    for (int b = 0; b < key_bits; ++b) {
+      const bool bit = (key >> b) & 1;
+      const uint64_t m = __ballot(bit);
+      same &= bit ? m : ~m;
+    }
+    const int rank = __popcll(same & ((uint64_t(1) << lane) - 1));
+    int old = 0;
+    if (live && rank == 0) old = atomicAdd(&mine[key], __popcll(same));  // one lane per key
+    old = __shfl(old, live ? __ffsll((unsigned long long)same) - 1 : lane);
+    tag[it] = key | (old + rank) << 11;
+  }
+  __syncthreads();
+
+  // this lane's bins b0 .. b0 + bpt - 1: waves scanned in place, then the bins
+  const int bpt = (nb + SORT_THREADS - 1) / SORT_THREADS;
+  const int b0 = tid * bpt;
+  int before[SORT_BPT], total[SORT_BPT], sum = 0;
+#pragma unroll
+  for (int u = 0; u < SORT_BPT; ++u) {
+    before[u] = total[u] = 0;
+    const int b = b0 + u;
+    if (u < bpt && b < nb) {
+      int run = 0;
+#pragma unroll
+      for (int w = 0; w < SORT_WAVES; ++w) {
+        const int c = hist[w * nb + b];
+        hist[w * nb + b] = run;
+        run += c;
+      }
+      total[u] = run;
+      if (nblk > 1) {
+        int all = 0, pre = 0;
+#pragma unroll 8
+        for (int q = 0; q < nblk; ++q) {
+          const int c = counts[(int64_t)q * nb + b];
+          all += c;
+          pre += q < blk ? c : 0;
+        }
+        total[u] = all;
+        before[u] = pre;
+      }
+      sum += total[u];
+    }
+  }
+  int incl = sum;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int v = __shfl_up(incl, d);
+    incl += lane >= d ? v : 0;
+  }
+  if (lane == 63) wave_sum[wave] = incl;
+  __syncthreads();
+  int start = incl - sum;
+#pragma unroll
+  for (int w = 0; w < SORT_WAVES; ++w) start += w < wave ? wave_sum[w] : 0;
+#pragma unroll
+  for (int u = 0; u < SORT_BPT; ++u) {
+    const int b = b0 + u;
+    if (u < bpt && b < nb) {
+      if (blk == 0) offsets[b] = start;
+#pragma unroll
+      for (int w = 0; w < SORT_WAVES; ++w) hist[w * nb + b] += start + before[u];
+      start += total[u];
+    }
+  }
+  __syncthreads();
+
+#pragma unroll
+  for (int it = 0; it < SORT_IT; ++it) {
+    const int s = s0 + it * 64;
+    if (s < slots) {
+      const int key = tag[it] & 2047;
+      const int pos = mine[key] + (tag[it] >> 11);
+      order[pos] = s;
+      place[s] = key == bins ? -1 : pos;
+    }
+  }
+}
+
+// --------------------------------------------------------------- the moves
+//
+// Bound by HBM.  A lane holds 16 bytes of a token's row.  Rows of any length and
+// alignment take the same path: global loads and stores of 16 bytes need no
+// more than the element's own alignment on gfx950, and the last lane of a row
+// takes what is left element by element.
+enum { DT_F32 = 0, DT_F16 = 1, DT_BF16 = 2 };
+
+template <int DT> constexpr int elem_bytes() { return DT == DT_F32 ? 4 : 2; }
+template <int DT> constexpr int per_lane() { return 16 / elem_bytes<DT>(); }
+
+struct alignas(2) Raw16 { uint16_t h[8]; };
+
+// elements [e, e + per_lane) of a row of h elements; past the end: zero bits
+template <int DT>
+__device__ __forceinline__ uint4 load16(const uint8_t* row, int64_t e, int64_t h) {
+  constexpr int VE = per_lane<DT>(), EB = elem_bytes<DT>();
+  uint4 v = make_uint4(0, 0, 0, 0);
+  if (e + VE <= h) {
+    __builtin_memcpy(&v, reinterpret_cast<const Raw16*>(row + e * EB), 16);
+  } else {
+    uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < VE; ++i)
+      if (e + i < h) {
+        if (DT == DT_F32) w[i] = *reinterpret_cast<const uint32_t*>(row + (e + i) * 4);
+        else w[i / 2] |= (uint32_t)*reinterpret_cast<const uint16_t*>(row + (e + i) * 2) << (16 * (i % 2));
+      }
+    v = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  return v;
+}
+
+template <int DT>
+__device__ __forceinline__ void store16(uint8_t* row, int64_t e, int64_t h, uint4 v) {
+  constexpr int VE = per_lane<DT>(), EB = elem_bytes<DT>();
+  if (e + VE <= h) {
+    __builtin_memcpy(reinterpret_cast<Raw16*>(row + e * EB), &v, 16);
+  } else {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < VE; ++i)
+      if (e + i < h) {
+        if (DT == DT_F32) *reinterpret_cast<uint32_t*>(row + (e + i) * 4) = w[i];
+        else *reinterpret_cast<uint16_t*>(row + (e + i) * 2) = (uint16_t)(w[i / 2] >> (16 * (i % 2)));
+      }
+  }
+}
+
+template <int DT>
+__device__ __forceinline__ void unpack(uint4 v, float (&f)[per_lane<DT>()]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < per_lane<DT>(); ++i) {
+    if (DT == DT_F32) f[i] = __uint_as_float(w[i]);
+    else if (DT == DT_F16) f[i] = f16_to_f32((w[i / 2] >> (16 * (i % 2))) & 0xFFFFu);
+    else f[i] = bf16_to_f32((w[i / 2] >> (16 * (i % 2))) & 0xFFFFu);
+  }
+}
+
+// one rounding, to nearest even, NaN kept
+template <int DT>
+__device__ __forceinline__ uint4 pack(const float (&f)[per_lane<DT>()]) {
+  uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+  for (int i = 0; i < per_lane<DT>(); ++i) {
+    if (DT == DT_F32) w[i] = __float_as_uint(f[i]);
+    else if (DT == DT_F16) w[i / 2] |= f32_to_f16_rne(f[i]) << (16 * (i % 2));
+    else w[i / 2] |= (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)f[i]) << (16 * (i % 2));
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+struct MoveArgs {
+  const uint8_t* src;      // dispatch: x; combine: the sorted rows
+  const int* place;        // [t][topk]
+  const float* weights;    // combine: nullable
+  uint8_t* dst;
+  int64_t h;
+  int t, topk, slots;
+  int lane_bits;           // 2^lane_bits lanes of a workgroup share a token (at most 256)
+  int chunks;              // workgroups per token (1 when several tokens share one)
+};
+
+// the lane's token and first element; false past the end
+template <int DT>
+__device__ __forceinline__ bool move_lane(const MoveArgs& p, int& token, int64_t& e) {
+  const int unit = (int)(blockIdx.x / (unsigned)p.chunks), chunk = (int)(blockIdx.x % (unsigned)p.chunks);
+  token = unit * (256 >> p.lane_bits) + ((int)threadIdx.x >> p.lane_bits);
+  e = ((int64_t)chunk * 256 + (threadIdx.x & ((1 << p.lane_bits) - 1))) * per_lane<DT>();
+  return token < p.t && e < p.h;
+}
+
+template <int DT>
+__global__ __launch_bounds__(256) void k_dispatch_rows(MoveArgs p) {
+  int token;
+  int64_t e;
+  if (!move_lane<DT>(p, token, e)) return;
+  const int64_t pitch = p.h * elem_bytes<DT>();
+  const uint4 v = load16<DT>(p.src + token * pitch, e, p.h);
+  const int* pl = p.place + (int64_t)token * p.topk;
+  for (int j = 0; j < p.topk; ++j) {
+    const int pos = pl[j];
+    if ((unsigned)pos < (unsigned)p.slots) store16<DT>(p.dst + pos * pitch, e, p.h, v);
+  }
+}
+
+// Four rows in flight per lane; summed in float32 in the order of j.
+template <int DT, bool WEIGHTED>
+__global__ __launch_bounds__(256) void k_combine_rows(MoveArgs p) {
+  constexpr int VE = per_lane<DT>(), JB = 4;
+  int token;
+  int64_t e;
+  if (!move_lane<DT>(p, token, e)) return;
+  const int64_t pitch = p.h * elem_bytes<DT>();
+  const int64_t first = (int64_t)token * p.topk;
+  float acc[VE];
+#pragma unroll
+  for (int i = 0; i < VE; ++i) acc[i] = 0.f;
+  for (int j0 = 0; j0 < p.topk; j0 += JB) {
+    int pos[JB];
+    float w[JB];
+    uint4 raw[JB];
+#pragma unroll
+    for (int u = 0; u < JB; ++u) {
+      const bool on = j0 + u < p.topk;
+      pos[u] = on ? p.place[first + j0 + u] : -1;
+      w[u] = WEIGHTED && on ? p.weights[first + j0 + u] : 1.f;
+    }
+#pragma unroll
+    for (int u = 0; u < JB; ++u)
+      if ((unsigned)pos[u] < (unsigned)p.slots) raw[u] = load16<DT>(p.src + pos[u] * pitch, e, p.h);
+#pragma unroll
+    for (int u = 0; u < JB; ++u)
+      if ((unsigned)pos[u] < (unsigned)p.slots) {
+        float f[VE];
+        unpack<DT>(raw[u], f);
+#pragma unroll
+        for (int i = 0; i < VE; ++i) acc[i] = WEIGHTED ? fmaf(w[u], f[i], acc[i]) : acc[i] + f[i];
+      }
+  }
+  store16<DT>(p.dst + token * pitch, e, p.h, pack<DT>(acc));
+}
+
+struct GradArgs {
+  const uint8_t* d_out;
+  const uint8_t* rows;
+  const int* place;
+  const float* weights;
+  uint8_t* d_rows;
+  float* d_weights;
+  int64_t h;
+  int t, topk, slots;
+};
+
+// LANES (64 or 256) lanes walk one token's row; each 16 bytes of d_out meet up
+// to JB rows at a time: the scaled copy goes out, the product with the row
+// goes into that row's sum.  The sums join in a fixed order.
+template <int DT, int LANES>
+__global__ __launch_bounds__(256) void k_combine_rows_grad(GradArgs p) {
+  constexpr int VE = per_lane<DT>(), JB = 4, WAVES = LANES / 64;
+  __shared__ float part[WAVES > 1 ? WAVES : 1][JB];
+  const int token = (int)blockIdx.x * (256 / LANES) + (int)threadIdx.x / LANES;
+  if (token >= p.t) return;  // wave-uniform; with LANES = 256 the whole workgroup
+  const int l = threadIdx.x % LANES;
+  const int64_t pitch = p.h * elem_bytes<DT>();
+  const int64_t first = (int64_t)token * p.topk;
+  for (int j0 = 0; j0 < p.topk; j0 += JB) {
+    int pos[JB];
+    float w[JB], dot[JB];
+#pragma unroll
+    for (int u = 0; u < JB; ++u) {
+      const bool on = j0 + u < p.topk;
+      pos[u] = on ? p.place[first + j0 + u] : -1;
+      w[u] = on ? p.weights[first + j0 + u] : 0.f;
+      dot[u] = 0.f;
+    }
+    for (int64_t e = (int64_t)l * VE; e < p.h; e += LANES * VE) {
+      uint4 raw[JB];
+      const uint4 dv = load16<DT>(p.d_out + token * pitch, e, p.h);
+#pragma unroll
+      for (int u = 0; u < JB; ++u)
+        if ((unsigned)pos[u] < (unsigned)p.slots) raw[u] = load16<DT>(p.rows + pos[u] * pitch, e, p.h);
+      float d[VE];
+      unpack<DT>(dv, d);
+#pragma unroll
+      for (int u = 0; u < JB; ++u)
+        if ((unsigned)pos[u] < (unsigned)p.slots) {
+          float f[VE], g[VE];
+          unpack<DT>(raw[u], f);
+#pragma unroll
+          for (int i = 0; i < VE; ++i) {
+            g[i] = w[u] * d[i];
+            dot[u] = fmaf(d[i], f[i], dot[u]);
+          }
+          store16<DT>(p.d_rows + pos[u] * pitch, e, p.h, pack<DT>(g));
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < JB; ++u)
+#pragma unroll
+      for (int d = 32; d > 0; d >>= 1) dot[u] += __shfl_xor(dot[u], d);
+    if constexpr (WAVES > 1) {
+      if (l % 64 == 0)
+#pragma unroll
+        for (int u = 0; u < JB; ++u) part[l / 64][u] = dot[u];
+      __syncthreads();
+      if (l < JB && j0 + l < p.topk) {
+        float s = 0.f;
+#pragma unroll
+        for (int q = 0; q < WAVES; ++q) s += part[q][l];
+        p.d_weights[first + j0 + l] = s;
+      }
+      __syncthreads();
+    } else if (l == 0) {
+#pragma unroll
+      for (int u = 0; u < JB; ++u)
+        if (j0 + u < p.topk) p.d_weights[first + j0 + u] = dot[u];
+    }
+  }
+}
+
+template <int DT>
+unsigned move_grid(MoveArgs& p) {
+  const int64_t nv = (p.h + per_lane<DT>() - 1) / per_lane<DT>();
+  p.lane_bits = 8;
+  while (p.lane_bits > 0 && (int64_t(1) << (p.lane_bits - 1)) >= nv) --p.lane_bits;
+  p.chunks = (int)((nv + 255) / 256);
+  const int per = 256 >> p.lane_bits;
+  return (unsigned)(((int64_t)p.t + per - 1) / per * p.chunks);
+}
+
+template <int DT>
+hipError_t dispatch(MoveArgs p, hipStream_t s) {
+  const unsigned grid = move_grid<DT>(p);
+  hipLaunchKernelGGL(k_dispatch_rows<DT>, dim3(grid), dim3(256), 0, s, p);
+  return hipGetLastError();
+}
+
+template <int DT>
+hipError_t combine(MoveArgs p, hipStream_t s) {
+  const unsigned grid = move_grid<DT>(p);
+  if (p.weights) hipLaunchKernelGGL((k_combine_rows<DT, true>), dim3(grid), dim3(256), 0, s, p);
+  else hipLaunchKernelGGL((k_combine_rows<DT, false>), dim3(grid), dim3(256), 0, s, p);
+  return hipGetLastError();
+}
+
+template <int DT>
+hipError_t combine_grad(const GradArgs& p, hipStream_t s) {
+  // a wave walks a row of up to two of its strides; longer rows take a workgroup
+  if (p.h <= 128 * per_lane<DT>())
+    hipLaunchKernelGGL((k_combine_rows_grad<DT, 64>), dim3((unsigned)((p.t + 3) / 4)), dim3(256), 0, s, p);
+  else
+    hipLaunchKernelGGL((k_combine_rows_grad<DT, 256>), dim3((unsigned)p.t), dim3(256), 0, s, p);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+size_t sort_rows_workspace(int64_t slots, int64_t bins) {
+  const int64_t blocks = (slots + SORT_CHUNK - 1) / SORT_CHUNK;
+  return blocks > 1 ? (size_t)(blocks * (bins + 1)) * sizeof(int) : 0;
+}
+
+hipError_t launch_sort_rows(const int32_t* ids, int64_t slots, int64_t bins, int32_t* offsets, int32_t* order,
+                            int32_t* place, void* ws, hipStream_t s) {
+  const unsigned blocks = slots > 0 ? (unsigned)((slots + SORT_CHUNK - 1) / SORT_CHUNK) : 1u;
+  int bits = 1;
+  while ((bins >> bits) != 0) ++bits;  // keys 0 .. bins
+  if (blocks > 1) {
+    hipLaunchKernelGGL(k_sort_count, dim3(blocks), dim3(SORT_THREADS), 0, s, ids, (int)slots, (int)bins,
+                       (int*)ws);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  hipLaunchKernelGGL(k_sort_place, dim3(blocks), dim3(SORT_THREADS), 0, s, ids, (int)slots, (int)bins, bits,
+                     (const int*)ws, offsets, order, place);
+  return hipGetLastError();
+}
+
+hipError_t launch_dispatch_rows(const void* x, int dtype, const int32_t* place, int64_t t, int64_t topk, int64_t h,
+                                void* out, hipStream_t s) {
+  MoveArgs p{};
+  p.src = (const uint8_t*)x;
+  p.place = place;
+  p.dst = (uint8_t*)out;
+  p.h = h;
+  p.t = (int)t;
+  p.topk = (int)topk;
+  p.slots = (int)(t * topk);
+  return dtype == DT_F32 ? dispatch<DT_F32>(p, s) : dispatch<DT_F16>(p, s);  // 2-byte types: the bits alone
+}
+
+hipError_t launch_combine_rows(const void* rows, int dtype, const int32_t* place, const float* weights, int64_t t,
+                               int64_t topk, int64_t h, void* out, hipStream_t s) {
+  MoveArgs p{};
+  p.src = (const uint8_t*)rows;
+  p.place = place;
+  p.weights = weights;
+  p.dst = (uint8_t*)out;
+  p.h = h;
+  p.t = (int)t;
+  p.topk = (int)topk;
+  p.slots = (int)(t * topk);
+  return dtype == DT_F32 ? combine<DT_F32>(p, s) : dtype == DT_F16 ? combine<DT_F16>(p, s) : combine<DT_BF16>(p, s);
+}
+
+hipError_t launch_combine_rows_grad(const void* d_out, const void* rows, int dtype, const int32_t* place,
+                                    const float* weights, int64_t t, int64_t topk, int64_t h, void* d_rows,
+                                    float* d_weights, hipStream_t s) {
+  GradArgs p;
+  p.d_out = (const uint8_t*)d_out;
+  p.rows = (const uint8_t*)rows;
+  p.place = place;
+  p.weights = weights;
+  p.d_rows = (uint8_t*)d_rows;
+  p.d_weights = d_weights;
+  p.h = h;
+  p.t = (int)t;
+  p.topk = (int)topk;
+  p.slots = (int)(t * topk);
+  return dtype == DT_F32   ? combine_grad<DT_F32>(p, s)
+         : dtype == DT_F16 ? combine_grad<DT_F16>(p, s)
+                           : combine_grad<DT_BF16>(p, s);
+}
+
+}  // namespace wq

@@ -156,4 +156,18 @@ hipError_t launch_gemv_ternary_sb(const uint8_t* w, const uint8_t* codebook, con
                                   const uint8_t* esc_patt, int64_t n_esc, const uint8_t* xq, bool pt,
                                   int64_t n, int64_t k, int64_t c, float* out, hipStream_t s);
 
+// Rows sorted by bin and moved there and back (route_rows.hip).
+constexpr int kMaxBins = 1024;                 // per-wave counters of a sort fit LDS
+constexpr int64_t kMaxSlots = int64_t(1) << 24;  // t * topk
+size_t sort_rows_workspace(int64_t slots, int64_t bins);
+hipError_t launch_sort_rows(const int32_t* ids, int64_t slots, int64_t bins, int32_t* offsets, int32_t* order,
+                            int32_t* place, void* ws, hipStream_t s);
+hipError_t launch_dispatch_rows(const void* x, int dtype, const int32_t* place, int64_t t, int64_t topk, int64_t h,
+                                void* out, hipStream_t s);
+hipError_t launch_combine_rows(const void* rows, int dtype, const int32_t* place, const float* weights, int64_t t,
+                               int64_t topk, int64_t h, void* out, hipStream_t s);
+hipError_t launch_combine_rows_grad(const void* d_out, const void* rows, int dtype, const int32_t* place,
+                                    const float* weights, int64_t t, int64_t topk, int64_t h, void* d_rows,
+                                    float* d_weights, hipStream_t s);
+
 }  // namespace wq

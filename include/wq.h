@@ -339,6 +339,80 @@ int wq_gemv_ternary_ptq1_1_pt(const uint8_t* superblocks, const uint8_t* codeboo
                               const uint8_t* x_pt, int64_t n, int64_t k, int64_t c, float* out,
                               void* stream);
 
+/*
+ * Rows that go to different weights
+ * ------------------------------------------------------------------------
+ *  A slot is one choice of one token: slot = token * topk + j.  Its id names
+ *  the bin (expert, adapter) that the row goes to; an id outside [0, bins)
+ *  drops the slot.  wq_sort_rows gives the plan that the calls below share:
+ *    offsets [bins + 1] int32: bin b owns sorted rows offsets[b] ..
+ *            offsets[b + 1] - 1; offsets[bins] is the number of kept slots.
+ *    order   [t * topk] int32: the slot of each sorted row, slots of one bin
+ *            in ascending order, the dropped slots behind the last bin.
+ *    place   [t * topk] int32: the sorted row of each slot, -1 if dropped.
+ *  The calls read the plan on the device.  Positions outside their arrays are
+ *  skipped as dropped ones are, so a plan that was never written cannot make
+ *  them leave their buffers, but its results then mean nothing.
+ */
+
+/*
+ * wq_sort_rows_workspace -- bytes of workspace that wq_sort_rows needs for
+ * these sizes (0 for small ones; a negative wq_status if the sizes are not
+ * accepted).
+ */
+int64_t wq_sort_rows_workspace(int64_t t, int64_t topk, int64_t bins);
+
+/*
+ * wq_sort_rows -- stable sort of slots by bin.
+ *   ids       [t][topk] int32, any values.
+ *   offsets, order, place   out, as above; every element is written.
+ *   workspace device memory of wq_sort_rows_workspace() bytes that nothing
+ *             else uses until the call has run (NULL if that is 0).  Two
+ *             captured graphs that may run at once need one each.
+ * The result is a function of ids alone.  t == 0 writes offsets (all 0).
+ * Requires 1 <= bins <= 1024, t * topk <= 2^24, pointers 4-byte aligned; a
+ * workspace that is too small is WQ_EINVAL.
+ */
+int wq_sort_rows(const int32_t* ids, int64_t t, int64_t topk, int64_t bins, int32_t* offsets, int32_t* order,
+                 int32_t* place, void* workspace, int64_t workspace_bytes, void* stream);
+
+/*
+ * wq_dispatch_rows -- out[place[i][j]] = x[i]: every token's row to its bins.
+ *   x     [t][h], dtype WQ_F32, WQ_F16 or WQ_BF16 (copied bit for bit).
+ *   place [t][topk] int32 from wq_sort_rows.
+ *   out   [t * topk][h]; rows that no slot goes to (behind offsets[bins])
+ *         are left as they were.
+ * Its gradient with respect to x is wq_combine_rows of out's gradient with
+ * weights NULL.  Requires t * topk <= 2^24, h < 2^31, x and out aligned to
+ * the element.
+ */
+int wq_dispatch_rows(const void* x, int dtype, const int32_t* place, int64_t t, int64_t topk, int64_t h, void* out,
+                     void* stream);
+
+/*
+ * wq_combine_rows -- out[i] = sum_j weights[i][j] * rows[place[i][j]]: the way
+ * back.
+ *   rows    [t * topk][h], out [t][h], dtype WQ_F32, WQ_F16 or WQ_BF16.
+ *   weights [t][topk] float32, or NULL for 1.
+ * Summed in float32 in the order of j, rounded once (RNE).  Dropped slots add
+ * nothing, whatever their weight; a token with none left gives zeros.
+ * Requirements as wq_dispatch_rows.  out must not overlap rows.
+ */
+int wq_combine_rows(const void* rows, int dtype, const int32_t* place, const float* weights, int64_t t, int64_t topk,
+                    int64_t h, void* out, void* stream);
+
+/*
+ * wq_combine_rows_grad -- gradients of wq_combine_rows (weights required):
+ *   d_rows[place[i][j]] = weights[i][j] * d_out[i]         [t * topk][h]
+ *   d_weights[i][j]     = <d_out[i], rows[place[i][j]]>    [t][topk] float32
+ * Products and sums in float32, d_rows rounded once to dtype (that of d_out
+ * and rows).  A dropped slot's weight gets 0; rows of d_rows behind the kept
+ * ones are left as they were.  Bitwise repeatable.  Requirements as
+ * wq_dispatch_rows; d_rows must not overlap d_out (it may be rows itself).
+ */
+int wq_combine_rows_grad(const void* d_out, const void* rows, int dtype, const int32_t* place, const float* weights,
+                         int64_t t, int64_t topk, int64_t h, void* d_rows, float* d_weights, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -25,4 +25,4 @@ pinned only by invariants (not by a value printed on the pages) say
 nibble order, the ternary digit encoding and the PTQ1_1 bit positions and
 codebook order (pinned by round trips, sizes and hand-worked bytes only).
 """
-from . import fpformat, int4, ternary  # noqa: F401
+from . import fpformat, int4, routing, ternary  # noqa: F401

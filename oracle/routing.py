@@ -1,0 +1,69 @@
+"""Oracle for rows that go to different weights: the sort by bin, the moves
+there and back with their gradients, the experts' int4 products and the
+low-rank adapters.
+
+TEST INFRASTRUCTURE (see ``oracle/__init__``): plain loops over the
+definitions in float64, written apart from the HIP path.  The pages do not
+define these operators (parity unpinned); the definitions are this library's,
+pinned by hand-worked cases and invariants in ``tests/test_oracle_routing.py``.
+"""
+from __future__ import annotations
+
+import numpy as np
+
+from . import int4
+
+
+def sort_rows(ids: np.ndarray, bins: int):
+    """ids [t][topk] -> (offsets [bins + 1], order [slots], place [t][topk]):
+    slot = i * topk + j; slots of one bin ascending, bins in order, dropped
+    slots (id outside [0, bins)) behind them in ascending order with place -1."""
+    flat = np.asarray(ids).reshape(-1)
+    lists = [[] for _ in range(bins + 1)]
+    for slot, b in enumerate(flat.tolist()):
+        lists[b if 0 <= b < bins else bins].append(slot)
+    offsets = np.zeros(bins + 1, dtype=np.int32)
+    for b in range(bins):
+        offsets[b + 1] = offsets[b] + len(lists[b])
+    order = np.array([s for one in lists for s in one], dtype=np.int32).reshape(-1)
+    place = np.full(flat.size, -1, dtype=np.int32)
+    for i in range(int(offsets[bins])):
+        place[order[i]] = i
+    return offsets, order, place.reshape(np.asarray(ids).shape)
+
+
+def dispatch_rows(x: np.ndarray, place: np.ndarray, out: np.ndarray) -> np.ndarray:
+    """A copy of ``out`` with out[place[i][j]] = x[i] for every kept slot."""
+    out = np.array(out)
+    for i, row in enumerate(place):
+        for p in row:
+            if p >= 0:
+                out[p] = x[i]
+    return out
+
+
+def combine_rows(rows: np.ndarray, place: np.ndarray, weights) -> np.ndarray:
+    """out[i] = sum_j weights[i][j] * rows[place[i][j]] (weights None: 1)."""
+    t, topk = place.shape
+    out = np.zeros((t, rows.shape[1]), dtype=np.float64)
+    for i in range(t):
+        for j in range(topk):
+            if place[i, j] >= 0:
+                w = 1.0 if weights is None else float(weights[i, j])
+                out[i] += w * rows[place[i, j]].astype(np.float64)
+    return out
+
+
+def combine_rows_grad(d_out, rows, place, weights, d_rows):
+    """(d_rows, d_weights): a copy of ``d_rows`` with d_rows[place[i][j]] =
+    weights[i][j] * d_out[i], and d_weights[i][j] = <d_out[i], rows[place[i][j]]>
+    (0 for a dropped slot)."""
+    d_rows = np.array(d_rows, dtype=np.float64)
+    d_w = np.zeros(place.shape, dtype=np.float64)
+    for i, row in enumerate(place):
+        d = d_out[i].astype(np.float64)
+        for j, p in enumerate(row):
+            if p >= 0:
+                d_rows[p] = float(weights[i, j]) * d
+                d_w[i, j] = float(np.dot(d, rows[p].astype(np.float64)))
+    return d_rows, d_w

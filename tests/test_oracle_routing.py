@@ -1,0 +1,72 @@
+"""Pins of the routed-rows oracle: hand-worked cases, brute force and
+invariants (the definitions are not on the pages)."""
+import numpy as np
+import pytest
+
+from oracle import routing
+
+
+def test_sort_hand_worked():
+    # slots 0..7 of four tokens; bin 1 stays empty, -1 and 3 are dropped
+    ids = np.array([[2, 0], [0, -1], [2, 2], [3, 0]])
+    offsets, order, place = routing.sort_rows(ids, 3)
+    assert offsets.tolist() == [0, 3, 3, 6]
+    assert order.tolist() == [1, 2, 7, 0, 4, 5, 3, 6]
+    assert place.tolist() == [[3, 0], [1, -1], [4, 5], [-1, 2]]
+
+
+@pytest.mark.parametrize("t,topk,bins", [(0, 2, 3), (1, 1, 1), (5, 8, 2), (200, 3, 17)])
+def test_sort_invariants(t, topk, bins):
+    rng = np.random.default_rng(t + topk)
+    ids = rng.integers(-2, bins + 2, size=(t, topk))
+    offsets, order, place = routing.sort_rows(ids, bins)
+    flat = ids.reshape(-1)
+    assert sorted(order.tolist()) == list(range(t * topk))
+    assert offsets[0] == 0 and offsets[-1] == np.count_nonzero((flat >= 0) & (flat < bins))
+    for b in range(bins):
+        mine = order[offsets[b]:offsets[b + 1]]
+        assert np.array_equal(mine, np.flatnonzero(flat == b))
+        assert np.array_equal(place.reshape(-1)[mine], np.arange(offsets[b], offsets[b + 1]))
+    assert np.all(place.reshape(-1)[order[offsets[-1]:]] == -1)
+
+
+def test_moves_hand_worked():
+    x = np.array([[1.0, 2.0], [3.0, 4.0]])
+    place = np.array([[1, -1], [0, 2]])
+    out = routing.dispatch_rows(x, place, np.full((4, 2), 9.0))
+    assert out.tolist() == [[3, 4], [1, 2], [3, 4], [9, 9]]
+    back = routing.combine_rows(out, place, np.array([[2.0, 5.0], [0.5, -1.0]]))
+    assert back.tolist() == [[2, 4], [-1.5, -2]]
+    assert routing.combine_rows(out, place, None).tolist() == [[1, 2], [6, 8]]
+    d_rows, d_w = routing.combine_rows_grad(np.array([[1.0, 1.0], [1.0, 0.0]]), out, place,
+                                            np.array([[2.0, 5.0], [0.5, -1.0]]), np.full((4, 2), 7.0))
+    assert d_rows.tolist() == [[0.5, 0], [2, 2], [-1, 0], [7, 7]]
+    assert d_w.tolist() == [[3, 0], [3, 3]]
+
+
+def test_gradients_by_differences():
+    # combine is linear in the rows and in the weights: a central difference of
+    # <d_out, combine> is its gradient up to rounding
+    rng = np.random.default_rng(0)
+    t, topk, h = 4, 3, 5
+    _, _, place = routing.sort_rows(rng.integers(-1, 4, size=(t, topk)), 4)
+    rows, w, d = rng.normal(size=(t * topk, h)), rng.normal(size=(t, topk)), rng.normal(size=(t, h))
+    d_rows, d_w = routing.combine_rows_grad(d, rows, place, w, np.zeros((t * topk, h)))
+
+    def value(rows, w):
+        return float(np.sum(d * routing.combine_rows(rows, place, w)))
+    eps = 1e-3
+    for i in range(t * topk):
+        for k in range(h):
+            step = np.zeros_like(rows)
+            step[i, k] = eps
+            assert abs((value(rows + step, w) - value(rows - step, w)) / (2 * eps) - d_rows[i, k]) < 1e-9
+    for i in range(t):
+        for j in range(topk):
+            step = np.zeros_like(w)
+            step[i, j] = eps
+            assert abs((value(rows, w + step) - value(rows, w - step)) / (2 * eps) - d_w[i, j]) < 1e-9
+    # dispatch's gradient is the unweighted combine: <r, dispatch(x)> = <combine(r), x>
+    x = rng.normal(size=(t, h))
+    moved = routing.dispatch_rows(x, place, np.zeros((t * topk, h)))
+    assert abs(np.sum(moved * rows) - np.sum(x * routing.combine_rows(rows, place, None))) < 1e-9
