@@ -44,6 +44,7 @@ _SIGS = {
     "wq_dispatch_rows": ([_p, _i, _p, _i64, _i64, _i64, _p, _p], _i),
     "wq_combine_rows": ([_p, _i, _p, _p, _i64, _i64, _i64, _p, _p], _i),
     "wq_combine_rows_grad": ([_p, _p, _i, _p, _p, _i64, _i64, _i64, _p, _p, _p], _i),
+    "wq_gemm_w4a16_experts": ([_p, _i64, _p, _i64, _p, _i64, _i64, _p, _i, _p, _p, _i64, _f, _i64, _i64, _p, _p], _i),
     # calibration kernels (include/wq_peaks.h)
     "wq_peak_read_sink_words": ([], _i64),
     "wq_peak_read": ([_p, _i64, _p, _i64, _p], _i),
@@ -443,6 +444,36 @@ def wq_combine_rows_grad(d_out, rows, place, weights, d_rows, d_weights, stream=
     d = st.device
     _call("wq_combine_rows_grad", st, _ptr(d_out, d), _ptr(rows, d), _dtype(rows, _ROW_DTYPES), _ptr(place, d),
           _ptr(weights, d), t, topk, h, _ptr(d_rows, d), _ptr(d_weights, d))
+
+
+def wq_gemm_w4a16_experts(a, order, topk, offsets, b, layout, scales, zeros, group, zero_const, c_out, stream=None):
+    """Rows sorted by expert times their experts' weights: c_out bf16 [slots][n]
+    from a bf16 and b uint8 [e][n][k/2], scales (and zeros, or None for
+    zero_const) bf16 [e][n][k/group], offsets int32 [e + 1].  With order
+    (int32 [slots]) a holds the tokens' rows [slots / topk][k]; without it the
+    sorted rows [slots][k]."""
+    _require(a.dim() == 2 and c_out.dim() == 2 and b.dim() == 3, "a is [rows][k], c_out [slots][n], b [e][n][k/2]")
+    a_rows, k = a.shape
+    e, n, slots = b.shape[0], b.shape[1], c_out.shape[0]
+    _require(a.dtype == torch.bfloat16 and c_out.dtype == torch.bfloat16, "a and c_out are bf16")
+    _require(b.dtype == torch.uint8 and b.shape[2] * 2 == k, "b is uint8 [e][n][k/2]")
+    _require(c_out.shape[1] == n, "c_out is [slots][n]")
+    _require(scales.dtype == torch.bfloat16, "scales are bf16")
+    _require(group > 0 and scales.numel() == e * n * (k // group), "scales hold e * n * (k / group) values")
+    if zeros is not None:
+        _require(zeros.dtype == torch.bfloat16 and zeros.numel() == scales.numel(), "zeros are bf16 of the scales' shape")
+    _plan_i32(offsets)
+    _require(offsets.numel() == e + 1, "offsets hold e + 1 values")
+    if order is not None:
+        _plan_i32(order)
+        _require(topk > 0 and order.numel() == slots and a_rows * topk == slots,
+                 "with order, a is [slots / topk][k] and order [slots]")
+    else:
+        _require(a_rows == slots, "without order, a is [slots][k]")
+    st = _stream(stream)
+    d = st.device
+    _call("wq_gemm_w4a16_experts", st, _ptr(a, d), a_rows, _ptr(order, d), topk, _ptr(offsets, d), slots, e,
+          _ptr(b, d), layout, _ptr(scales, d), _ptr(zeros, d), group, float(zero_const), n, k, _ptr(c_out, d))
 
 
 # ---- calibration kernels (include/wq_peaks.h): practical ceilings of the

@@ -331,4 +331,28 @@ int wq_combine_rows_grad(const void* d_out, const void* rows, int dtype, const i
                                                  as_stream(stream)));
 }
 
+int wq_gemm_w4a16_experts(const uint16_t* a, int64_t a_rows, const int32_t* order, int64_t topk,
+                          const int32_t* offsets, int64_t slots, int64_t experts, const uint8_t* b, int layout,
+                          const uint16_t* scales, const uint16_t* zeros, int64_t group, float zero_const, int64_t n,
+                          int64_t k, uint16_t* c_out, void* stream) {
+  if (a_rows < 0 || topk < 0 || slots < 0 || experts < 0 || n < 0 || k < 0 || group < 0) return WQ_EINVAL;
+  if (layout != WQ_LAYOUT_PLAIN && layout != WQ_LAYOUT_GFX950) return WQ_EINVAL;
+  if (slots == 0 || n == 0) return WQ_OK;
+  if (!a || !offsets || !b || !scales || !c_out) return WQ_EINVAL;
+  if (experts < 1 || experts > wq::kMaxBins || slots > wq::kMaxSlots) return WQ_ESHAPE;
+  if (k == 0 || k % 64 != 0 || k > (int64_t(1) << 22) || !valid_group(group, k)) return WQ_ESHAPE;
+  // without order the rows are taken as they lie; with it a_rows tokens of topk slots each
+  if (order ? topk < 1 || mul_sat(a_rows, topk) != slots : a_rows != slots) return WQ_ESHAPE;
+  if (mul_sat(n, experts) >= (int64_t(1) << 31)) return WQ_ESHAPE;
+  if (order && mul_sat(a_rows, 2 * k) >= (int64_t(1) << 31)) return WQ_ESHAPE;  // 32-bit offsets of the gather
+  if (mul_sat(wq::row_tiles_bound(slots, experts, 4), n / 16 + 1) > kMaxGrid) return WQ_ESHAPE;
+  if (group < 64) return WQ_EUNSUPPORTED;  // a 64-k step must lie in one group
+  if (layout != WQ_LAYOUT_GFX950) return WQ_EUNSUPPORTED;
+  if (!aligned(a, 16) || !aligned(b, 16) || !aligned(c_out, 16) || !aligned(scales, 4) || !aligned(zeros, 4) ||
+      !aligned(order, 4) || !aligned(offsets, 4))
+    return WQ_EALIGN;
+  return hip_status(wq::launch_gemm_w4a16_experts(a, a_rows, order, topk, offsets, slots, experts, b, scales, zeros,
+                                                  group, zero_const, n, k, c_out, as_stream(stream)));
+}
+
 }  // extern "C"

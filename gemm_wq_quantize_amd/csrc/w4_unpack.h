@@ -1,0 +1,98 @@
+// Packed int4 codes to bf16 matrix-core operands (gfx950 layout), shared by the
+// W4A16 GEMM and the experts' products.
+#pragma once
+
+#include "wq_internal.h"
+
+namespace wq {
+
+__device__ __forceinline__ uint32_t and_or(uint32_t x, uint32_t mask_s, uint32_t bits_v) {
+  uint32_t r;
+  asm("v_and_or_b32 %0, %1, %2, %3" : "=v"(r) : "v"(x), "s"(mask_s), "v"(bits_v));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t vconst(uint32_t c) {
+  uint32_t r;
+  asm volatile("v_mov_b32 %0, %1" : "=v"(r) : "i"(c));
+  return r;
+}
+
+// eight codes of one gfx950-layout word -> bf16x8 of (128 + q), k order
+__device__ __forceinline__ bf16x8 unpack8(uint32_t w, uint32_t magic_v) {
+  typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+  u32x4 r;
+  r[0] = and_or(w, 0x000F000Fu, magic_v);
+  r[1] = and_or(w >> 4, 0x000F000Fu, magic_v);
+  r[2] = and_or(w >> 8, 0x000F000Fu, magic_v);
+  r[3] = and_or(w >> 12, 0x000F000Fu, magic_v);
+  return __builtin_bit_cast(bf16x8, r);
+}
+
+// byte b of v as float32: v_cvt_f32_ubyte{0..3} (written out: the compiler
+// otherwise extracts the byte with a separate v_bfe_u32)
+__device__ __forceinline__ float cvt_ubyte(uint32_t v, int b) {
+  float r;
+  if (b == 0) asm("v_cvt_f32_ubyte0 %0, %1" : "=v"(r) : "v"(v));
+  else if (b == 1) asm("v_cvt_f32_ubyte1 %0, %1" : "=v"(r) : "v"(v));
+  else if (b == 2) asm("v_cvt_f32_ubyte2 %0, %1" : "=v"(r) : "v"(v));
+  else asm("v_cvt_f32_ubyte3 %0, %1" : "=v"(r) : "v"(v));
+  return r;
+}
+
+// eight codes of one gfx950-layout word -> bf16x8 of (q - z) * s, k order,
+// with c = -z * s.  Nibble p holds element {0,2,4,6,1,3,5,7}[p]; the even
+// nibbles masked in place are the bytes of elements 0, 4, 1, 5, the odd ones
+// shifted down those of 2, 6, 3, 7, and each byte converts to float with one
+// v_cvt_f32_ubyteN.  q * s + c is exact in float32 (bf16 s, and z an integer
+// or bf16, so z * s and the sum need at most 17 significant bits), so the
+// only rounding is the one to bf16 (v_cvt_pk_bf16_f32).
+__device__ __forceinline__ bf16x8 unpack8_scaled(uint32_t w, float s, float c) {
+  typedef __bf16 bf2 __attribute__((ext_vector_type(2)));
+  typedef float f2 __attribute__((ext_vector_type(2)));
+  typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+  const uint32_t ev = w & 0x0F0F0F0Fu;         // bytes: elements 0, 4, 1, 5
+  const uint32_t od = (w >> 4) & 0x0F0F0F0Fu;  // bytes: elements 2, 6, 3, 7
+  auto ub = [](uint32_t v, int b) { return cvt_ubyte(v, b); };
+  const float e[8] = {ub(ev, 0), ub(ev, 2), ub(od, 0), ub(od, 2), ub(ev, 1), ub(ev, 3), ub(od, 1), ub(od, 3)};
+  u32x4 r;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const f2 v = {fmaf(e[2 * j], s, c), fmaf(e[2 * j + 1], s, c)};
+    r[j] = __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf2));
+  }
+  return __builtin_bit_cast(bf16x8, r);
+}
+
+// The same eight weights with the codes taken as fp16 magic numbers: a nibble
+// masked into the low mantissa bits under 0x6400 (1024) reads 1024 + q, one
+// masked into bits 4..7 reads 1024 + 16 q, so four v_and_or_b32 and one
+// shift give all eight codes as fp16 halves, and v_fma_mix_f32 (fp16 source,
+// fp32 scale and addend) forms (1024 + q) * s + c0 and (1024 + 16 q) * s/16 +
+// c1 with c0 = -(1024 + z) * s and c1 = -(64 + z) * s.  Both equal (q - z) * s
+// exactly when z is a multiple of 2^-5 below 1024 in magnitude (the products
+// need at most 19 significant bits and the addends at most 24), so the
+// results are those of unpack8_scaled: 17 VALU instructions per word instead
+// of 23.
+__device__ __forceinline__ bf16x8 unpack8_scaled_mix(uint32_t w, float s, float s16, float c0, float c1,
+                                                     uint32_t magic_v) {
+  typedef __bf16 bf2 __attribute__((ext_vector_type(2)));
+  typedef float f2 __attribute__((ext_vector_type(2)));
+  typedef _Float16 h2 __attribute__((ext_vector_type(2)));
+  typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+  const uint32_t t = w >> 8;
+  const h2 p[4] = {__builtin_bit_cast(h2, and_or(w, 0x000F000Fu, magic_v)),   // elements 0, 1
+                   __builtin_bit_cast(h2, and_or(w, 0x00F000F0u, magic_v)),   // 2, 3 (x 16)
+                   __builtin_bit_cast(h2, and_or(t, 0x000F000Fu, magic_v)),   // 4, 5
+                   __builtin_bit_cast(h2, and_or(t, 0x00F000F0u, magic_v))};  // 6, 7 (x 16)
+  u32x4 r;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float sj = (j & 1) ? s16 : s, cj = (j & 1) ? c1 : c0;
+    const f2 v = {fmaf((float)p[j].x, sj, cj), fmaf((float)p[j].y, sj, cj)};
+    r[j] = __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf2));
+  }
+  return __builtin_bit_cast(bf16x8, r);
+}
+
+}  // namespace wq

@@ -159,6 +159,12 @@ hipError_t launch_gemv_ternary_sb(const uint8_t* w, const uint8_t* codebook, con
 // Rows sorted by bin and moved there and back (route_rows.hip).
 constexpr int kMaxBins = 1024;                 // per-wave counters of a sort fit LDS
 constexpr int64_t kMaxSlots = int64_t(1) << 24;  // t * topk
+// Upper bound of the tiles of 2^shift rows that `rows` sorted rows in `bins`
+// bins make: every bin adds at most one partial tile.
+inline int64_t row_tiles_bound(int64_t rows, int64_t bins, int shift) {
+  const int64_t most = (rows >> shift) + bins;
+  return most < rows ? most : rows;
+}
 size_t sort_rows_workspace(int64_t slots, int64_t bins);
 hipError_t launch_sort_rows(const int32_t* ids, int64_t slots, int64_t bins, int32_t* offsets, int32_t* order,
                             int32_t* place, void* ws, hipStream_t s);
@@ -169,5 +175,11 @@ hipError_t launch_combine_rows(const void* rows, int dtype, const int32_t* place
 hipError_t launch_combine_rows_grad(const void* d_out, const void* rows, int dtype, const int32_t* place,
                                     const float* weights, int64_t t, int64_t topk, int64_t h, void* d_rows,
                                     float* d_weights, hipStream_t s);
+
+// The experts' int4 products (gemm_experts.hip); order nullable, a_rows rows in a.
+hipError_t launch_gemm_w4a16_experts(const uint16_t* a, int64_t a_rows, const int32_t* order, int64_t topk,
+                                     const int32_t* offsets, int64_t slots, int64_t experts, const uint8_t* b,
+                                     const uint16_t* scales, const uint16_t* zeros, int64_t group, float zero_const,
+                                     int64_t n, int64_t k, uint16_t* c, hipStream_t s);
 
 }  // namespace wq

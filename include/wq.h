@@ -413,6 +413,40 @@ int wq_combine_rows(const void* rows, int dtype, const int32_t* place, const flo
 int wq_combine_rows_grad(const void* d_out, const void* rows, int dtype, const int32_t* place, const float* weights,
                          int64_t t, int64_t topk, int64_t h, void* d_rows, float* d_weights, void* stream);
 
+/*
+ * wq_gemm_w4a16_experts -- rows sorted by expert times their experts' int4
+ * weights: C[i][j] = sum_k A[src(i)][k] * (q[e][j][k] - z) * s[e][j][k / group]
+ * for expert e and its rows i = offsets[e] .. offsets[e + 1] - 1.
+ *   a       bf16, a_rows rows of k.  order NULL: src(i) = i, a_rows = slots.
+ *           order given: src(i) = order[i] / topk, so a holds the tokens'
+ *           rows (a_rows = slots / topk) and is gathered on the way in.
+ *   order   [slots] int32 and offsets [experts + 1] int32 from wq_sort_rows
+ *           (slots = t * topk, topk >= 1; topk is not used without order).
+ *   b       [experts][n][k/2] uint8 in `layout` (WQ_LAYOUT_GFX950 only).
+ *   scales  [experts][n][k/group] bf16; group a power of two with 64 <= group
+ *           dividing k, or k (one scale per column).
+ *   zeros   NULL (then every zero point is zero_const) or bf16 of the scales'
+ *           shape.
+ *   c_out   [slots][n] bf16 (RNE); rows behind offsets[experts] are left as
+ *           they were.
+ * One row or many: the kernel is chosen from slots, experts, n and k alone, and
+ * reads only the weights of experts that have rows.  Accumulates in float32.
+ * Finite a, scales and zeros are assumed.  Where many rows share an
+ * expert each weight is first rounded to bf16((q - z) * s) as in
+ * wq_gemm_w4a16; with few rows, and with one scale per column, no weight is
+ * rounded (one scale per column: if q - z is exact in bf16, as it is for
+ * integer zeros).
+ * Bitwise repeatable.  Requires k % 64 == 0, k <= 2^22, slots <= 2^24,
+ * 1 <= experts <= 1024, n * experts < 2^31, a gathered `a` below 2 GiB;
+ * a, b and c_out 16-byte aligned, scales and zeros 4-byte (whole aligned
+ * 4-byte words are read, so the 2 bytes after the last element may be read
+ * and are ignored).
+ */
+int wq_gemm_w4a16_experts(const uint16_t* a, int64_t a_rows, const int32_t* order, int64_t topk,
+                          const int32_t* offsets, int64_t slots, int64_t experts, const uint8_t* b, int layout,
+                          const uint16_t* scales, const uint16_t* zeros, int64_t group, float zero_const, int64_t n,
+                          int64_t k, uint16_t* c_out, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -67,3 +67,20 @@ def combine_rows_grad(d_out, rows, place, weights, d_rows):
                 d_rows[p] = float(weights[i, j]) * d
                 d_w[i, j] = float(np.dot(d, rows[p].astype(np.float64)))
     return d_rows, d_w
+
+
+def gemm_experts(a, order, topk, offsets, packed, scales, zeros, zero_const, group, out, bf16_weights=False):
+    """A copy of ``out`` [slots][n] whose rows offsets[e] .. offsets[e + 1] - 1
+    hold a[src(i)] times expert e's weights (packed [e][n][k/2] in the gfx950
+    layout); src(i) = order[i] // topk, or i without ``order``.
+    ``bf16_weights``: each weight rounded to bf16 first."""
+    out = np.array(out, dtype=np.float64)
+    for e in range(packed.shape[0]):
+        lo, hi = int(offsets[e]), int(offsets[e + 1])
+        if lo == hi:
+            continue
+        src = np.arange(lo, hi) if order is None else np.asarray(order[lo:hi]) // topk
+        z = None if zeros is None else zeros[e]
+        rows = int4.gemm_w4a16_rows_bf16w if bf16_weights else int4.gemm_w4a16_rows
+        out[lo:hi] = rows(a[src], packed[e], int4.LAYOUT_GFX950, scales[e], zero_const, group, zeros=z)
+    return out

@@ -86,3 +86,38 @@ def test_binding_refusals():
         g.wq_combine_rows_grad(z((4, 16), bf), z((8, 16), bf), ids, z((4, 2), f32), z((8, 16), bf), z((4, 1), f32))
     with pytest.raises(ValueError, match="sorted rows"):
         g.wq_combine_rows_grad(z((4, 16), bf), z((8, 16), bf), ids, z((4, 2), f32), z((8, 15), bf), z((4, 2), f32))
+
+
+def test_experts_refusals(lib):
+    def f(a=FAKE, rows=4, order=FAKE, topk=2, off=FAKE, slots=8, e=3, b=FAKE, layout=1, s=FAKE, zr=None, group=128,
+          n=40, k=256, c=FAKE):
+        return lib.wq_gemm_w4a16_experts(a, rows, order, topk, off, slots, e, b, layout, s, zr, group, 8.0, n, k, c,
+                                         None)
+    assert f(a=None, off=None, slots=0, rows=0) == g.WQ_OK and f(a=None, n=0) == g.WQ_OK
+    for kw in (dict(a=None), dict(off=None), dict(b=None), dict(s=None), dict(c=None), dict(rows=-1), dict(e=-1),
+               dict(layout=2), dict(k=-64)):
+        assert f(**kw) == g.WQ_EINVAL, kw
+    for kw in (dict(e=0), dict(e=1025), dict(k=0), dict(k=96, group=96), dict(k=(1 << 22) + 64), dict(group=96),
+               dict(group=512), dict(rows=3), dict(topk=0), dict(order=None, rows=4), dict(n=1 << 30),
+               dict(rows=1 << 23, slots=1 << 24), dict(rows=1 << 24, topk=2, slots=1 << 25)):
+        assert f(**kw) == g.WQ_ESHAPE, kw
+    assert f(order=None, rows=1 << 25, slots=1 << 25) == g.WQ_ESHAPE
+    assert f(rows=(1 << 31) // (2 * 8192), topk=1, slots=(1 << 31) // (2 * 8192), k=8192) == g.WQ_ESHAPE
+    assert f(layout=0) == g.WQ_EUNSUPPORTED and f(group=32) == g.WQ_EUNSUPPORTED
+    for kw in (dict(a=ODD), dict(b=P(0x1008)), dict(c=P(0x1008)), dict(s=HALF), dict(zr=HALF), dict(order=HALF),
+               dict(off=HALF)):
+        assert f(**kw) == g.WQ_EALIGN, kw
+
+
+def test_experts_binding_refusals():
+    i32, bf, u8 = torch.int32, torch.bfloat16, torch.uint8
+    args = dict(a=z((4, 256), bf), order=z(8, i32), topk=2, offsets=z(4, i32), b=z((3, 40, 128), u8), layout=1,
+                scales=z((3, 40, 2), bf), zeros=None, group=128, zero_const=8.0, c_out=z((8, 40), bf))
+    for kw, match in ((dict(a=z((4, 256), torch.float32)), "bf16"), (dict(b=z((3, 40, 127), u8)), "b is uint8"),
+                      (dict(c_out=z((8, 39), bf)), "c_out"), (dict(scales=z((3, 40, 1), bf)), "scales"),
+                      (dict(scales=z((3, 40, 2), torch.float32)), "scales"), (dict(group=0), "scales"),
+                      (dict(zeros=z((3, 40, 1), bf)), "zeros"), (dict(offsets=z(3, i32)), "offsets"),
+                      (dict(offsets=z(4, torch.int64)), "int32"), (dict(order=z(7, i32)), "order"),
+                      (dict(topk=1), "order"), (dict(order=None), "without order")):
+        with pytest.raises(ValueError, match=match):
+            g.wq_gemm_w4a16_experts(**{**args, **kw})

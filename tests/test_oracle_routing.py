@@ -3,7 +3,7 @@ invariants (the definitions are not on the pages)."""
 import numpy as np
 import pytest
 
-from oracle import routing
+from oracle import int4, routing
 
 
 def test_sort_hand_worked():
@@ -70,3 +70,27 @@ def test_gradients_by_differences():
     x = rng.normal(size=(t, h))
     moved = routing.dispatch_rows(x, place, np.zeros((t * topk, h)))
     assert abs(np.sum(moved * rows) - np.sum(x * routing.combine_rows(rows, place, None))) < 1e-9
+
+
+@pytest.mark.parametrize("topk,gather,zeros", [(1, True, False), (2, True, True), (3, False, False)])
+def test_experts_brute_force(topk, gather, zeros):
+    rng = np.random.default_rng(topk)
+    t, e, n, k, group = 5, 4, 3, 128, 64
+    offsets, order, _ = routing.sort_rows(rng.integers(-1, e, size=(t, topk)), e)
+    codes = rng.integers(0, 16, size=(e, n, k)).astype(np.uint8)
+    packed = np.stack([int4.pack(c, int4.LAYOUT_GFX950) for c in codes])
+    scales = rng.uniform(0.5, 2, size=(e, n, k // group))
+    z = rng.uniform(6, 9, size=scales.shape) if zeros else None
+    a = rng.normal(size=(t if gather else t * topk, k))
+    got = routing.gemm_experts(a, order if gather else None, topk, offsets, packed, scales, z, 8.0, group,
+                               np.full((t * topk, n), 4.0))
+    for i in range(t * topk):
+        if i >= offsets[e]:
+            assert np.all(got[i] == 4.0)
+            continue
+        b = [x for x in range(e) if offsets[x] <= i < offsets[x + 1]][0]
+        src = order[i] // topk if gather else i
+        for j in range(n):
+            want = sum(a[src, x] * (int(codes[b, j, x]) - (z[b, j, x // group] if zeros else 8.0)) *
+                       scales[b, j, x // group] for x in range(k))
+            assert abs(got[i, j] - want) < 1e-9
