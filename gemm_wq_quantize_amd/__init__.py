@@ -45,6 +45,8 @@ _SIGS = {
     "wq_combine_rows": ([_p, _i, _p, _p, _i64, _i64, _i64, _p, _p], _i),
     "wq_combine_rows_grad": ([_p, _p, _i, _p, _p, _i64, _i64, _i64, _p, _p, _p], _i),
     "wq_gemm_w4a16_experts": ([_p, _i64, _p, _i64, _p, _i64, _i64, _p, _i, _p, _p, _i64, _f, _i64, _i64, _p, _p], _i),
+    "wq_lora_workspace": ([_i64, _i64, _i64, _i64], _i64),
+    "wq_lora": ([_p, _i64, _i64, _p, _p, _i64, _p, _p, _i64, _p, _p, _p, _i, _i64, _p, _i64, _p], _i),
     # calibration kernels (include/wq_peaks.h)
     "wq_peak_read_sink_words": ([], _i64),
     "wq_peak_read": ([_p, _i64, _p, _i64, _p], _i),
@@ -474,6 +476,40 @@ def wq_gemm_w4a16_experts(a, order, topk, offsets, b, layout, scales, zeros, gro
     d = st.device
     _call("wq_gemm_w4a16_experts", st, _ptr(a, d), a_rows, _ptr(order, d), topk, _ptr(offsets, d), slots, e,
           _ptr(b, d), layout, _ptr(scales, d), _ptr(zeros, d), group, float(zero_const), n, k, _ptr(c_out, d))
+
+
+def wq_lora_workspace(t, k, adapters, rank):
+    """Bytes of workspace that wq_lora needs for these sizes."""
+    need = lib.wq_lora_workspace(t, k, adapters, rank)
+    if need < 0:
+        raise WqError("wq_lora_workspace", need)
+    return need
+
+
+def wq_lora(x, order, offsets, a, b, scales, base, out, workspace=None, stream=None):
+    """out[i] = base[i] + scales[l] * b[l] (a[l] x[i]) for the adapter l of row i:
+    x bf16 [t][k], a bf16 [l][rank][k], b bf16 [l][n][rank], scales fp32 [l],
+    base (or None) and out [t][n] fp32 or bf16 (out may be base); order and
+    offsets from wq_sort_rows over the rows' adapters."""
+    _require(x.dim() == 2 and a.dim() == 3 and b.dim() == 3 and out.dim() == 2,
+             "x is [t][k], a [l][rank][k], b [l][n][rank], out [t][n]")
+    t, k = x.shape
+    n_ad, rank, n = a.shape[0], a.shape[1], b.shape[1]
+    _require(x.dtype == torch.bfloat16 and a.dtype == torch.bfloat16 and b.dtype == torch.bfloat16,
+             "x, a and b are bf16")
+    _require(a.shape[2] == k and b.shape[0] == n_ad and b.shape[2] == rank, "a is [l][rank][k] and b [l][n][rank]")
+    _require(tuple(out.shape) == (t, n), "out is [t][n]")
+    if base is not None:
+        _require(base.dtype == out.dtype and tuple(base.shape) == (t, n), "base matches out in dtype and shape")
+    _require(scales.dtype == torch.float32 and scales.numel() == n_ad, "scales are fp32, one an adapter")
+    _plan_i32(order, offsets)
+    _require(order.numel() == t and offsets.numel() == n_ad + 1, "order holds t values, offsets adapters + 1")
+    st = _stream(stream)
+    d = st.device
+    args = (_ptr(x, d), t, k, _ptr(order, d), _ptr(offsets, d), n_ad, _ptr(a, d), _ptr(b, d), rank, _ptr(scales, d),
+            _ptr(base, d), _ptr(out, d), _dtype(out), n)
+    ws, nbytes = _workspace("wq_lora", st, workspace, lib.wq_lora_workspace(t, k, n_ad, rank))
+    _call("wq_lora", st, *args, _ptr(ws, d), nbytes)
 
 
 # ---- calibration kernels (include/wq_peaks.h): practical ceilings of the

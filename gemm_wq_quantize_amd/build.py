@@ -18,7 +18,7 @@ LIB = os.path.join(HERE, "libwq.so")
 OBJDIR = os.path.join(HERE, "_build")
 
 SOURCES = ["capi.cpp", "ptq1_1.cpp", "quantize_pack.hip", "gemv_w4.hip", "gemm_w4a16.hip", "ternary.hip",
-           "route_rows.hip", "gemm_experts.hip", "peaks.hip"]
+           "route_rows.hip", "gemm_experts.hip", "lora.hip", "peaks.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [

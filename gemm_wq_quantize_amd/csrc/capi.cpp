@@ -355,4 +355,31 @@ int wq_gemm_w4a16_experts(const uint16_t* a, int64_t a_rows, const int32_t* orde
                                                   group, zero_const, n, k, c_out, as_stream(stream)));
 }
 
+int64_t wq_lora_workspace(int64_t t, int64_t k, int64_t adapters, int64_t rank) {
+  if (t < 0 || k < 0 || adapters < 0 || rank < 0) return WQ_EINVAL;
+  if (t > wq::kMaxSlots || adapters < 1 || adapters > wq::kMaxBins) return WQ_ESHAPE;
+  if (rank < 8 || rank % 8 != 0 || rank > wq::kMaxRank) return WQ_ESHAPE;
+  if (k == 0 || k % 32 != 0 || k > (int64_t(1) << 24)) return WQ_ESHAPE;
+  return (int64_t)wq::lora_workspace(t, adapters, rank, k);
+}
+
+int wq_lora(const uint16_t* x, int64_t t, int64_t k, const int32_t* order, const int32_t* offsets, int64_t adapters,
+            const uint16_t* a, const uint16_t* b, int64_t rank, const float* scales, const void* base, void* out,
+            int out_dtype, int64_t n, void* workspace, int64_t workspace_bytes, void* stream) {
+  if (t < 0 || n < 0 || (out_dtype != WQ_F32 && out_dtype != WQ_BF16)) return WQ_EINVAL;
+  const int64_t need = wq_lora_workspace(t, k, adapters, rank);
+  if (need < 0) return (int)need;
+  if (t == 0 || n == 0) return WQ_OK;
+  if (!x || !order || !offsets || !a || !b || !scales || !out || !workspace) return WQ_EINVAL;
+  if (workspace_bytes < need) return WQ_EINVAL;
+  if (n >= (int64_t(1) << 31) || mul_sat(wq::row_tiles_bound(t, adapters + 1, 4), n / 128 + 1) > kMaxGrid)
+    return WQ_ESHAPE;
+  const uintptr_t es = (uintptr_t)dtype_size(out_dtype);
+  if (!aligned(x, 16) || !aligned(a, 16) || !aligned(b, 16) || !aligned(workspace, 16) || !aligned(order, 4) ||
+      !aligned(offsets, 4) || !aligned(scales, 4) || !aligned(base, es) || !aligned(out, es))
+    return WQ_EALIGN;
+  return hip_status(wq::launch_lora(x, t, k, order, offsets, adapters, a, b, rank, scales, base, out,
+                                    out_dtype == WQ_BF16, n, workspace, as_stream(stream)));
+}
+
 }  // extern "C"

@@ -182,4 +182,11 @@ hipError_t launch_gemm_w4a16_experts(const uint16_t* a, int64_t a_rows, const in
                                      const uint16_t* scales, const uint16_t* zeros, int64_t group, float zero_const,
                                      int64_t n, int64_t k, uint16_t* c, hipStream_t s);
 
+// Low-rank adapters beside a projection (lora.hip); ws of lora_workspace bytes.
+constexpr int kMaxRank = 128;
+size_t lora_workspace(int64_t t, int64_t adapters, int64_t rank, int64_t k);
+hipError_t launch_lora(const uint16_t* x, int64_t t, int64_t k, const int32_t* order, const int32_t* offsets,
+                       int64_t adapters, const uint16_t* a, const uint16_t* b, int64_t rank, const float* scales,
+                       const void* base, void* out, bool out_bf16, int64_t n, void* ws, hipStream_t s);
+
 }  // namespace wq

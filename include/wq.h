@@ -447,6 +447,37 @@ int wq_gemm_w4a16_experts(const uint16_t* a, int64_t a_rows, const int32_t* orde
                           const uint16_t* scales, const uint16_t* zeros, int64_t group, float zero_const, int64_t n,
                           int64_t k, uint16_t* c_out, void* stream);
 
+/*
+ * wq_lora_workspace -- bytes of workspace that wq_lora needs (a negative
+ * wq_status if the sizes are not accepted).
+ */
+int64_t wq_lora_workspace(int64_t t, int64_t k, int64_t adapters, int64_t rank);
+
+/*
+ * wq_lora -- low-rank adapters of many requests beside a shared projection:
+ * out[i] = base[i] + scales[l] * b[l] (a[l] x[i]), l = the adapter of row i.
+ *   x       [t][k] bf16.
+ *   order, offsets   from wq_sort_rows over the rows' adapters (topk = 1, bins
+ *           = adapters); rows whose id it dropped have no adapter: out = base.
+ *   a       [adapters][rank][k] bf16, b [adapters][n][rank] bf16.
+ *   scales  [adapters] float32.
+ *   base    [t][n], or NULL for zeros: the output of wq_gemv_w4 or
+ *           wq_gemm_w4a16 for the same x.
+ *   out     [t][n], may be base itself; out_dtype WQ_BF16 or WQ_F32, base has
+ *           the same.
+ *   workspace as for wq_sort_rows, wq_lora_workspace() bytes.
+ * Sums in float32, rounded once; a[l] x is carried to the second product with
+ * 17 significant bits for bf16 out, all 24 for float32.  Finite x, a, b and
+ * scales are assumed for rows that have an adapter; those without are copied
+ * bit for bit.  Bitwise repeatable.
+ * Requires k % 32 == 0, rank a multiple of 8 up to 128, 1 <= adapters <= 1024,
+ * t <= 2^24, n < 2^31, k <= 2^24; x, a, b and workspace 16-byte aligned, base
+ * and out to the element.
+ */
+int wq_lora(const uint16_t* x, int64_t t, int64_t k, const int32_t* order, const int32_t* offsets, int64_t adapters,
+            const uint16_t* a, const uint16_t* b, int64_t rank, const float* scales, const void* base, void* out,
+            int out_dtype, int64_t n, void* workspace, int64_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -84,3 +84,13 @@ def gemm_experts(a, order, topk, offsets, packed, scales, zeros, zero_const, gro
         rows = int4.gemm_w4a16_rows_bf16w if bf16_weights else int4.gemm_w4a16_rows
         out[lo:hi] = rows(a[src], packed[e], int4.LAYOUT_GFX950, scales[e], zero_const, group, zeros=z)
     return out
+
+
+def lora(x, ids, a, b, scales, base):
+    """out[i] = base[i] + scales[l] * b[l] (a[l] x[i]) with l = ids[i]; base[i]
+    alone where ids[i] names no adapter."""
+    out = np.array(base, dtype=np.float64)
+    for i, l in enumerate(np.asarray(ids).reshape(-1).tolist()):
+        if 0 <= l < a.shape[0]:
+            out[i] += float(scales[l]) * (b[l].astype(np.float64) @ (a[l].astype(np.float64) @ x[i].astype(np.float64)))
+    return out

@@ -121,3 +121,39 @@ def test_experts_binding_refusals():
                       (dict(topk=1), "order"), (dict(order=None), "without order")):
         with pytest.raises(ValueError, match=match):
             g.wq_gemm_w4a16_experts(**{**args, **kw})
+
+
+def test_lora_refusals(lib):
+    ws = lib.wq_lora_workspace
+    assert ws(1, 4096, 8, 16) > 0 and ws(0, 64, 1, 8) == 0
+    assert ws(-1, 64, 1, 8) == g.WQ_EINVAL
+    for t, k, l, r in ((4, 48, 1, 8), (4, 0, 1, 8), (4, (1 << 24) + 32, 1, 8), (4, 64, 0, 8), (4, 64, 1025, 8),
+                       (4, 64, 1, 0), (4, 64, 1, 12), (4, 64, 1, 136), ((1 << 24) + 1, 64, 1, 8)):
+        assert ws(t, k, l, r) == g.WQ_ESHAPE
+
+    def f(x=FAKE, t=4, k=64, order=FAKE, off=FAKE, l=3, a=FAKE, b=FAKE, r=16, s=FAKE, base=FAKE, out=FAKE, dt=2, n=40,
+          w=FAKE, nb=1 << 40):
+        return lib.wq_lora(x, t, k, order, off, l, a, b, r, s, base, out, dt, n, w, nb, None)
+    assert f(t=0, x=None, out=None) == g.WQ_OK and f(n=0, out=None) == g.WQ_OK
+    for kw in (dict(x=None), dict(order=None), dict(off=None), dict(a=None), dict(b=None), dict(s=None),
+               dict(out=None), dict(w=None), dict(dt=1), dict(n=-1), dict(t=-1), dict(nb=255)):
+        assert f(**kw) == g.WQ_EINVAL, kw
+    for kw in (dict(k=40), dict(r=20), dict(r=256), dict(l=0), dict(n=1 << 31), dict(t=1 << 24, n=(1 << 31) - 1)):
+        assert f(**kw) == g.WQ_ESHAPE, kw
+    for kw in (dict(x=P(0x1008)), dict(a=HALF), dict(b=P(0x1008)), dict(w=P(0x1008)), dict(order=HALF), dict(off=ODD),
+               dict(s=HALF), dict(base=ODD), dict(out=ODD), dict(dt=0, out=HALF)):
+        assert f(**kw) == g.WQ_EALIGN, kw
+
+
+def test_lora_binding_refusals():
+    i32, bf, f32 = torch.int32, torch.bfloat16, torch.float32
+    args = dict(x=z((4, 64), bf), order=z(4, i32), offsets=z(4, i32), a=z((3, 16, 64), bf), b=z((3, 40, 16), bf),
+                scales=z(3, f32), base=z((4, 40), bf), out=z((4, 40), bf))
+    for kw, match in ((dict(x=z((4, 64), f32)), "bf16"), (dict(a=z((3, 16, 32), bf)), "a is"),
+                      (dict(b=z((2, 40, 16), bf)), "a is"), (dict(b=z((3, 40, 8), bf)), "a is"),
+                      (dict(out=z((4, 39), bf)), "out is"), (dict(base=z((4, 40), f32)), "base"),
+                      (dict(scales=z(2, f32)), "scales"), (dict(scales=z(3, bf)), "scales"),
+                      (dict(order=z(5, i32)), "order"), (dict(offsets=z(3, i32)), "offsets"),
+                      (dict(order=z(4, torch.int64)), "int32")):
+        with pytest.raises(ValueError, match=match):
+            g.wq_lora(**{**args, **kw})

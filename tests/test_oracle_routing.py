@@ -94,3 +94,12 @@ def test_experts_brute_force(topk, gather, zeros):
             want = sum(a[src, x] * (int(codes[b, j, x]) - (z[b, j, x // group] if zeros else 8.0)) *
                        scales[b, j, x // group] for x in range(k))
             assert abs(got[i, j] - want) < 1e-9
+
+
+def test_lora_hand_worked():
+    x = np.array([[1.0, 2.0], [3.0, 4.0], [5.0, 6.0]])
+    a = np.array([[[1.0, 0.0]], [[0.0, 1.0]]])          # rank 1: picks x[0], x[1]
+    b = np.array([[[10.0], [20.0]], [[1.0], [-1.0]]])
+    base = np.array([[0.5, 0.5], [0.0, 0.0], [7.0, 8.0]])
+    got = routing.lora(x, np.array([1, 0, -1]), a, b, np.array([0.5, 3.0]), base)
+    assert got.tolist() == [[6.5, -5.5], [15.0, 30.0], [7.0, 8.0]]
