@@ -8,6 +8,9 @@
 // the number of rows but not how they fall, so a launch covers the most row
 // tiles that they can make; each workgroup finds its tile from the offsets and
 // those past the last one return.
+#include <cmath>
+#include <type_traits>
+
 #include "route_tiles.h"
 #include "w4_unpack.h"
 
@@ -17,24 +20,28 @@ namespace {
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
-// ------------------------------------------------------ up to 16 rows a tile
+// -------------------------------------------------------------- few rows a tile
 //
-// Bound by the weights' bytes.  A workgroup computes 16 rows x 16 CB columns
-// with v_mfma_f32_16x16x32_bf16; its four waves take every fourth chunk of k
-// and join their sums in LDS.  Operands come from memory straight into
-// registers: a lane holds 8 LW consecutive k of one column (LW packed words)
-// and the same k of one row, so slot k of MFMA w is k = chunk + 8 LW (lane /
-// 16) + 8 w + (0..7) on both sides.
+// Bound by the weights' bytes.  A workgroup takes a tile of up to 16 rows and
+// 64 CB columns.  The rows sit in LDS, a slab of k at a time, so what flows
+// through the vector memory path is the packed weights alone: each of the four
+// waves streams 16 CB columns over all of k from memory straight into
+// registers, DEPTH chunks ahead (a chunk is 32 LW k: 16 LW bytes of each
+// column).  Products on v_mfma_f32_16x16x32_bf16: lane l holds 8 LW consecutive k
+// of column l % 16 (LW packed words) and reads the same k of row l % 16, so slot
+// k of MFMA w is k = chunk + 8 LW (l / 16) + 8 w + (0..7) on both sides.
 //
 // The codes enter the MFMA as 128 + q, exact in bf16, and a chunk lies in one
 // group, so
-//   sum_chunk A (q - z) s = s (sum A (128 + q) - (128 + z) sum A)
-// with the row sums from one more MFMA per word against ones: they arrive in
-// the accumulator's own layout.  No weight is rounded, and the unpacking is 7
-// VALU instructions a word instead of the 17 that scaling each weight takes.
+//   sum_chunk A (q - z) s = s (sum A (128 + q) - (128 + z) sum A).
+// The row sums are made once a slab (MFMAs against ones, the waves take turns)
+// and kept in LDS in the accumulators' own layout.  No weight is rounded, and
+// unpacking takes 7 VALU instructions a word where scaling each weight takes 17.
+// The loop over full groups of DEPTH chunks has no branch: with one around each
+// load and block the waves waited on every LDS read by itself.
 //
-// Rows past the tile's last and columns past n repeat the last one: their
-// results are not stored, and their loads hit the lines of the others.
+// Rows past the tile's last and columns past n repeat another one: their
+// results are not stored.
 struct EArgs {
   const uint16_t* a;
   const int* order;     // nullable: A's row of sorted row i is order[i] / topk
@@ -49,6 +56,8 @@ struct EArgs {
   int tiles_n;
   int ngroups;      // k / group
   int group_chunks; // chunks per group
+  int gshift;       // 64-k step t lies in group t >> gshift
+  int plain_codes;  // tiles: unpack q - z unscaled, the column's scale goes on the sum
 };
 
 // the row of A that sorted row i reads; a position outside A reads its row 0
@@ -62,27 +71,40 @@ template <int LW> struct Words;
 template <> struct Words<4> { typedef u32x4 type; };
 template <> struct Words<2> { typedef u32x2 type; };
 
-template <int CB, int LW, bool Z>
-struct Chunk {
-  typename Words<LW>::type w[CB];
-  bf16x8 a[LW];
-  uint16_t s[CB], z[CB];
-};
+// eight codes of one word -> bf16x8 of (128 + q), k order.  In plain code, not asm:
+// the compiler then keeps the wait states that a matrix instruction needs
+// between the vector instruction that wrote its operand and itself.
+__device__ __forceinline__ bf16x8 codes8(uint32_t w, uint32_t magic_v) {
+  u32x4 r;
+  r[0] = (w & 0x000F000Fu) | magic_v;
+  r[1] = ((w >> 4) & 0x000F000Fu) | magic_v;
+  r[2] = ((w >> 8) & 0x000F000Fu) | magic_v;
+  r[3] = ((w >> 12) & 0x000F000Fu) | magic_v;
+  return __builtin_bit_cast(bf16x8, r);
+}
+
+constexpr int DEPTH = 4;             // chunks in flight per wave; also the chunks one scale load covers
+constexpr int FEW_LDS = 40 * 1024;   // a slab of rows and its row sums: four workgroups on a CU
+constexpr int FEW_SHIFT = 4, FEW_ROWS = 1 << FEW_SHIFT;
+static_assert((FEW_LDS - FEW_ROWS * 16) / (FEW_ROWS * 256 + FEW_ROWS * 4) >= DEPTH, "a slab holds DEPTH chunks");
 
 template <int CB, int LW, bool Z>
-__global__ __launch_bounds__(256) void k_experts_rows16(EArgs p) {
+__global__ __launch_bounds__(256) void k_experts_few(EArgs p) {
   typedef typename Words<LW>::type words_t;
-  __shared__ __attribute__((aligned(16))) float part[4][CB][4][64];  // [wave][block][element][lane]
-  const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  constexpr int CH_K = 32 * LW, CH_BYTES = CH_K * 2;  // k of a chunk, bytes of it in a row of A
+  __shared__ __attribute__((aligned(16))) uint8_t smem[FEW_LDS];
+  __shared__ int src[FEW_ROWS];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int m = (int)(blockIdx.x / (unsigned)p.tiles_n), tn = (int)(blockIdx.x % (unsigned)p.tiles_n);
   RowTile t;
   int count;
-  if (!find_row_tile<false>(p.offsets, p.experts, p.slots, 4, m, t, count)) return;
+  if (!find_row_tile<false>(p.offsets, p.experts, p.slots, FEW_SHIFT, m, t, count)) return;
 
+  // ---- the weights' first chunks are on their way before anything else
   const int lr = lane & 15, lq = lane >> 4;
-  const int64_t n0 = (int64_t)tn * (16 * CB);
-  const uint16_t* arow = p.a + a_row(p, t.row0 + min(lr, t.rows - 1)) * p.k + lq * (8 * LW);
+  const int64_t n0 = ((int64_t)tn * 4 + wave) * (16 * CB);
+  const int nch = (int)(p.k / CH_K);
   const uint8_t* brow[CB];
   int64_t srow[CB];
 #pragma unroll
@@ -91,79 +113,411 @@ __global__ __launch_bounds__(256) void k_experts_rows16(EArgs p) {
     brow[j] = p.b + col * (p.k / 2) + lq * (4 * LW);
     srow[j] = col * p.ngroups;
   }
-  auto load = [&](int ch, Chunk<CB, LW, Z>& f) {
-    const int64_t g = ch / p.group_chunks;
+  words_t w[DEPTH][CB];
+  uint16_t sc[2][CB], zc[2][CB];  // lane quarter q: the scale (zero) of chunk 4 (ch / 4) + q
+  auto load = [&](int ch, words_t (&f)[CB]) {
+#pragma unroll
+    for (int j = 0; j < CB; ++j) f[j] = *reinterpret_cast<const words_t*>(brow[j] + (int64_t)ch * (CH_K / 2));
+  };
+  auto load_s = [&](int ch, uint16_t (&s)[CB], uint16_t (&z)[CB]) {
+    const int64_t g = min(ch + lq, nch - 1) / p.group_chunks;
 #pragma unroll
     for (int j = 0; j < CB; ++j) {
-      f.w[j] = *reinterpret_cast<const words_t*>(brow[j] + (int64_t)ch * (16 * LW));
-      f.s[j] = p.scales[srow[j] + g];
-      if (Z) f.z[j] = p.zeros[srow[j] + g];
+      s[j] = p.scales[srow[j] + g];
+      if (Z) z[j] = p.zeros[srow[j] + g];
     }
-#pragma unroll
-    for (int w = 0; w < LW; ++w)
-      f.a[w] = *reinterpret_cast<const bf16x8*>(arow + (int64_t)ch * (32 * LW) + w * 8);
   };
+#pragma unroll
+  for (int d = 0; d < DEPTH; ++d)
+    if (d < nch) load(d, w[d]);
+  load_s(0, sc[0], zc[0]);
+  if (tid < t.rows) src[tid] = (int)a_row(p, t.row0 + tid);
+  __syncthreads();
+
+  // ---- slabs: as many chunks (a multiple of DEPTH) as this tile's rows leave
+  // room for; a row's pitch is 16 bytes off a multiple of 128, so 16 rows' reads
+  // of one k fall in different banks
+  const int room = (FEW_LDS - t.rows * 16) / (t.rows * CH_BYTES + FEW_ROWS * 4);
+  const int slab = min(room, (nch + DEPTH - 1) / DEPTH * DEPTH) / DEPTH * DEPTH;
+  const int pitch = slab * CH_BYTES + 16;
+  float* rs = reinterpret_cast<float*>(smem + FEW_LDS) - slab * FEW_ROWS;  // [chunk][row], at the end
   const uint32_t magic_v = vconst(0x43004300u);
   const u32x4 ones_u = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
   const bf16x8 ones = __builtin_bit_cast(bf16x8, ones_u);
+  const uint8_t* a_rd = smem + min(lr, t.rows - 1) * pitch + lq * (16 * LW);
   floatx4 acc[CB];
 #pragma unroll
   for (int j = 0; j < CB; ++j) acc[j] = floatx4{0.f, 0.f, 0.f, 0.f};
-  auto fold = [&](const Chunk<CB, LW, Z>& f) {
-    floatx4 sum[CB], rs = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int j = 0; j < CB; ++j) sum[j] = floatx4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int w = 0; w < LW; ++w) {
-      rs = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f.a[w], ones, rs, 0, 0, 0);
-#pragma unroll
-      for (int j = 0; j < CB; ++j)
-        sum[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f.a[w], unpack8(f.w[j][w], magic_v), sum[j], 0, 0, 0);
-    }
-#pragma unroll
-    for (int j = 0; j < CB; ++j) {
-      const float s = bf16_to_f32(f.s[j]);
-      const float zb = 128.f + (Z ? bf16_to_f32(f.z[j]) : p.zero_const);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) acc[j][e] = fmaf(s, fmaf(-zb, rs[e], sum[j][e]), acc[j][e]);
-    }
-  };
-  // this wave's chunks, two ahead of use
-  const int nch = (int)(p.k / (32 * LW));
-  Chunk<CB, LW, Z> f0, f1;
-  if (wave < nch) load(wave, f0);
-  if (wave + 4 < nch) load(wave + 4, f1);
-  for (int ch = wave; ch < nch; ch += 8) {
-    fold(f0);
-    if (ch + 8 < nch) load(ch + 8, f0);
-    if (ch + 4 < nch) {
-      fold(f1);
-      if (ch + 12 < nch) load(ch + 12, f1);
-    }
-  }
 
-  // join the waves' sums: element e of lane l is row 4 (l / 16) + e, column l % 16
+  for (int c0 = 0; c0 < nch; c0 += slab) {
+    const int c1 = min(c0 + slab, nch);
+    if (c0 > 0) __syncthreads();  // every wave is done with the slab before
+    const int pieces = (c1 - c0) * (CH_BYTES / 16);
+    for (int q = tid; q < t.rows * pieces; q += 256) {
+      const int row = q / pieces, c = q % pieces;
+      const u32x4 v = *reinterpret_cast<const u32x4*>(p.a + src[row] * p.k + (int64_t)c0 * CH_K + c * 8);
+      *reinterpret_cast<u32x4*>(smem + row * pitch + c * 16) = v;
+    }
+    __syncthreads();
+    for (int ch = wave; ch < c1 - c0; ch += 4) {
+      floatx4 r = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int u = 0; u < LW; ++u)
+        r = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+            *reinterpret_cast<const bf16x8*>(a_rd + ch * CH_BYTES + u * 16), ones, r, 0, 0, 0);
+      if (lr == 0) *reinterpret_cast<floatx4*>(rs + ch * FEW_ROWS + lq * 4) = r;
+    }
+    __syncthreads();
+
+    // FULL: all DEPTH chunks and all that their loads fetch exist
+    auto group = [&](auto full, int ch) {
+      constexpr bool FULL = decltype(full)::value;
+      if (FULL || ch + DEPTH < nch) load_s(ch + DEPTH, sc[1], zc[1]);
+#pragma unroll
+      for (int d = 0; d < DEPTH; ++d) {
+        if (!FULL && ch + d >= c1) break;
+        const int at = ch + d - c0;
+        floatx4 sum[CB];
+#pragma unroll
+        for (int j = 0; j < CB; ++j) sum[j] = floatx4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int u = 0; u < LW; ++u) {
+          const bf16x8 a = *reinterpret_cast<const bf16x8*>(a_rd + at * CH_BYTES + u * 16);
+#pragma unroll
+          for (int j = 0; j < CB; ++j)
+            sum[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, codes8(w[d][j][u], magic_v), sum[j], 0, 0, 0);
+        }
+        if (FULL || ch + d + DEPTH < nch) load(ch + d + DEPTH, w[d]);
+        const floatx4 r = *reinterpret_cast<const floatx4*>(rs + at * FEW_ROWS + lq * 4);
+#pragma unroll
+        for (int j = 0; j < CB; ++j) {
+          const float s = bf16_to_f32((uint32_t)__shfl((int)sc[0][j], d * 16 + lr));
+          const float zb = 128.f + (Z ? bf16_to_f32((uint32_t)__shfl((int)zc[0][j], d * 16 + lr)) : p.zero_const);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[j][e] = fmaf(s, fmaf(-zb, r[e], sum[j][e]), acc[j][e]);
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < CB; ++j) {
+        sc[0][j] = sc[1][j];
+        if (Z) zc[0][j] = zc[1][j];
+      }
+    };
+    int ch = c0;
+    for (; ch + DEPTH <= c1 && ch + 2 * DEPTH <= nch; ch += DEPTH) group(std::true_type{}, ch);
+    for (; ch < c1; ch += DEPTH) group(std::false_type{}, ch);
+  }
+  // element e of lane l is row 4 (l / 16) + e, column l % 16
 #pragma unroll
   for (int j = 0; j < CB; ++j)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) part[wave][j][e][lane] = acc[j][e];
-  __syncthreads();
-  for (int i = threadIdx.x; i < CB * 256; i += 256) {
-    const int j = i >> 8, e = (i >> 6) & 3, l = i & 63;
-    const int row = 4 * (l >> 4) + e;
-    const int64_t col = n0 + j * 16 + (l & 15);
-    const float v = (part[0][j][e][l] + part[1][j][e][l]) + (part[2][j][e][l] + part[3][j][e][l]);
-    if (row < t.rows && col < p.n)
-      p.c[(int64_t)(t.row0 + row) * p.n + col] = __builtin_bit_cast(uint16_t, (__bf16)v);
-  }
+    for (int e = 0; e < 4; ++e) {
+      const int row = 4 * lq + e;
+      const int64_t col = n0 + j * 16 + lr;
+      if (row < t.rows && col < p.n)
+        p.c[(int64_t)(t.row0 + row) * p.n + col] = __builtin_bit_cast(uint16_t, (__bf16)acc[j][e]);
+    }
 }
 
 template <int CB, int LW>
-hipError_t launch_rows16(EArgs p, hipStream_t s) {
-  p.tiles_n = (int)((p.n + 16 * CB - 1) / (16 * CB));
-  const unsigned grid = (unsigned)(row_tiles_bound(p.slots, p.experts, 4) * p.tiles_n);
-  if (p.zeros) hipLaunchKernelGGL((k_experts_rows16<CB, LW, true>), dim3(grid), dim3(256), 0, s, p);
-  else hipLaunchKernelGGL((k_experts_rows16<CB, LW, false>), dim3(grid), dim3(256), 0, s, p);
+hipError_t launch_few(EArgs p, hipStream_t s) {
+  p.tiles_n = (int)((p.n + 64 * CB - 1) / (64 * CB));
+  const dim3 grid((unsigned)(row_tiles_bound(p.slots, p.experts, FEW_SHIFT) * p.tiles_n));
+  if (p.zeros) hipLaunchKernelGGL((k_experts_few<CB, LW, true>), grid, dim3(256), 0, s, p);
+  else hipLaunchKernelGGL((k_experts_few<CB, LW, false>), grid, dim3(256), 0, s, p);
+  return hipGetLastError();
+}
+
+// ------------------------------------------------------- tiles of many rows
+//
+// Bound by the matrix cores where an expert has hundreds of rows, by its
+// weights' bytes where it has tens.  A workgroup computes 32 MI rows x 256
+// columns, each of its four waves all rows x 64 columns (MI x 2 blocks of
+// v_mfma_f32_32x32x16_bf16), so every packed word is unpacked by one wave.  k
+// advances 64 a step through a three-stage LDS ring that buffer loads fill
+// directly: A's rows (gathered by per-lane offsets), B packed, and the 4-byte
+// word that holds each column's scale.  Inside a step lane half h of 16-k slice
+// s takes the 8 k of chunk 4 h + s on both sides, so a lane's four packed words
+// of a step are one 16-byte LDS read.  Each weight becomes bf16((q - z) s) as it
+// is unpacked; with one scale per column and a constant zero that leaves q - z
+// exact in bf16 it stays q - z and the scale goes on the sum.
+//
+// MI = 4 keeps two workgroups on a CU (75 KiB of LDS and 256 registers each):
+// one multiplies while the other waits at its barrier or starts its tile.
+constexpr int TN = 256, TK = 64, RING = 3;
+constexpr int TB_BYTES = TN * TK / 2, TS_BYTES = TN * 4;
+
+template <int MI, bool Z> constexpr int tile_stage() { return MI * 32 * TK * 2 + TB_BYTES + TS_BYTES * (Z ? 2 : 1); }
+template <int MI, bool Z> constexpr int tile_loads() { return MI + 2 + (Z ? 2 : 1); }
+// workgroups a CU holds by LDS
+template <int MI> constexpr int tile_wgs() { return MI == 4 ? 2 : 3; }
+constexpr int TC_PITCH = TN * 2 + 16;  // staged C row: rows 4 apart fall in different banks
+
+// A-tile swizzle: physical 16-byte column of k-chunk c in row r is c ^ tile_swz(r)
+__device__ __forceinline__ int tile_swz(int r) { return (r & 7) ^ ((r >> 3) & 1); }
+
+template <int MI, bool Z, bool MX>
+__global__ __launch_bounds__(256, tile_wgs<MI>()) void k_experts_tile(EArgs p) {
+  static_assert(!(Z && MX), "the fp16-magic unpacking serves a constant zero");
+  constexpr int BM = 32 * MI, NJ = 2;
+  constexpr int A_BYTES = BM * TK * 2, STAGE = tile_stage<MI, Z>(), LOADS = tile_loads<MI, Z>();
+  constexpr int SHIFT = MI == 4 ? 7 : 6;
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[RING * STAGE];
+
+  // ---- which tile: the workgroups that have one are numbered so that each XCD
+  // (8, dispatched round-robin) gets a compact run of them, bands of 8 row
+  // tiles by all columns, and shares A and B rows in its own L2
+  const int tiles_m = count_row_tiles(p.offsets, p.experts, p.slots, SHIFT);
+  const int nwg = tiles_m * p.tiles_n;
+  int id = blockIdx.x;
+  if (id >= nwg) return;
+  {
+    const int xcd = id & 7, each = nwg >> 3, rest = nwg & 7;
+    id = xcd * each + min(xcd, rest) + (id >> 3);
+  }
+  const int per_band = 8 * p.tiles_n;
+  const int first_m = id / per_band * 8, in_band = id % per_band;
+  const int band_rows = min(8, tiles_m - first_m);
+  const int tn = in_band / band_rows;
+  RowTile t;
+  int count;
+  if (!find_row_tile<false>(p.offsets, p.experts, p.slots, SHIFT, first_m + in_band % band_rows, t, count)) return;
+
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int col0 = wave * 64;
+  const int64_t n0 = (int64_t)tn * TN, en0 = (int64_t)t.bin * p.n + n0;
+  const int rows_b = (int)min((int64_t)TN, p.n - n0);
+  const uint32_t kbytes_a = (uint32_t)(p.k * 2), kbytes_b = (uint32_t)(p.k / 2);
+  const int nk = (int)(p.k / TK);
+
+  // descriptors: A's rows (all of a gathered A, below 2 GiB; else this tile's),
+  // B's and the scales' rows of this tile; columns past n read as zero
+  const intx4 ars = p.order ? make_rsrc(p.a, (uint32_t)p.a_rows * kbytes_a)
+                            : make_rsrc(p.a + (int64_t)t.row0 * p.k, (uint32_t)t.rows * kbytes_a);
+  const intx4 brs = make_rsrc(p.b + en0 * (p.k / 2), (uint32_t)rows_b * kbytes_b);
+  // scales as whole aligned words: an expert's first scale may be the upper half
+  const int64_t s0 = en0 * p.ngroups;
+  const int odd = (int)(s0 & 1);
+  const uint32_t s_bytes = ((uint32_t)(odd + rows_b * p.ngroups) * 2u + 3u) & ~3u;
+  const intx4 srs = make_rsrc(p.scales + (s0 - odd), s_bytes);
+  const intx4 zrs = make_rsrc(Z ? p.zeros + (s0 - odd) : p.scales, Z ? s_bytes : 0u);
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)smem;
+
+  // ---- who loads what: A slot 64 (4 i + wave) + lane is row slot / 8, physical
+  // column slot % 8; B slots are [row][half ^ (row / 8) % 2]; rows past the
+  // tile's last repeat it
+  uint32_t a_voff[MI];
+#pragma unroll
+  for (int i = 0; i < MI; ++i) {
+    const int s = (i * 4 + wave) * 64 + lane;
+    const int row = s >> 3, chunk = (s & 7) ^ tile_swz(row);
+    const int r = min(row, t.rows - 1);
+    a_voff[i] = (uint32_t)(p.order ? a_row(p, t.row0 + r) : (int64_t)r) * kbytes_a + (uint32_t)chunk * 16;
+  }
+  uint32_t b_voff[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int s = (h * 4 + wave) * 64 + lane;
+    const int row = s >> 1, half = (s & 1) ^ ((row >> 3) & 1);
+    b_voff[h] = (uint32_t)row * kbytes_b + (uint32_t)half * 16;
+  }
+  const uint32_t s_voff = (uint32_t)(odd + (wave * 64 + lane) * p.ngroups) * 2u;
+
+  // loads [first, last) of step kt into stage kt % 3: MI of A, 2 of B, the scale
+  // (and zero) word.  Steps past the end are issued at offsets past the
+  // descriptors and read nothing, so the loop has no branch.
+  auto issue_part = [&](int kt, int first, int last) {
+    const uint32_t st = lds0 + (uint32_t)(kt % RING) * STAGE;
+    const bool live = kt < nk;
+    const uint32_t ka = live ? (uint32_t)kt * (TK * 2) : 0x80000000u;
+    const uint32_t kb = live ? (uint32_t)kt * (TK / 2) : 0x80000000u;
+#pragma unroll
+    for (int i = 0; i < MI; ++i)
+      if (i >= first && i < last)
+        dma16(ars, a_voff[i] + ka, __builtin_amdgcn_readfirstlane(st + (uint32_t)(i * 4 + wave) * 1024));
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      if (MI + h >= first && MI + h < last)
+        dma16(brs, b_voff[h] + kb, __builtin_amdgcn_readfirstlane(st + A_BYTES + (uint32_t)(h * 4 + wave) * 1024));
+    const uint32_t so = live ? ((s_voff + (uint32_t)(kt >> p.gshift) * 2u) & ~3u) : 0x80000000u;
+    if (MI + 2 >= first && MI + 2 < last)
+      dma4(srs, so, __builtin_amdgcn_readfirstlane(st + A_BYTES + TB_BYTES + (uint32_t)wave * 256));
+    if (Z && MI + 3 >= first && MI + 3 < last)
+      dma4(zrs, so, __builtin_amdgcn_readfirstlane(st + A_BYTES + TB_BYTES + TS_BYTES + (uint32_t)wave * 256));
+  };
+  // full scheduling barriers keep the asm loads in their place in the program
+  // order; the scheduling groups below would move code across them
+  auto issue_fenced = [&](int kt, int first, int last) {
+    __builtin_amdgcn_sched_barrier(0);
+    issue_part(kt, first, last);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  constexpr int P1 = (LOADS + 2) / 3, P2 = P1 + (LOADS + 1) / 3;
+
+  floatx16 acc[MI][NJ];
+#pragma unroll
+  for (int i = 0; i < MI; ++i)
+#pragma unroll
+    for (int j = 0; j < NJ; ++j)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.f;
+  const int lr = lane & 31, lh = lane >> 5;
+  const uint32_t magic_v = vconst(0x64006400u);
+  const int a_sw = tile_swz(lr);
+  int b_rd[NJ];
+#pragma unroll
+  for (int j = 0; j < NJ; ++j) b_rd[j] = A_BYTES + ((col0 + j * 32 + lr) * 2 + (lh ^ ((lr >> 3) & 1))) * 16;
+
+  auto read_b = [&](int kt, uint4 (&bw)[NJ]) {
+    const uint8_t* st = smem + (kt % RING) * STAGE;
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) bw[j] = *reinterpret_cast<const uint4*>(st + b_rd[j]);
+  };
+  auto read_s = [&](int kt, uint32_t (&sw)[NJ], uint32_t (&zw)[NJ]) {
+    const uint8_t* st = smem + (kt % RING) * STAGE + A_BYTES + TB_BYTES;
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+      sw[j] = *reinterpret_cast<const uint32_t*>(st + (col0 + j * 32 + lr) * 4);
+      zw[j] = Z ? *reinterpret_cast<const uint32_t*>(st + TS_BYTES + (col0 + j * 32 + lr) * 4) : 0u;
+    }
+  };
+  const float zm0 = -(1024.f + p.zero_const), zm1 = -(64.f + p.zero_const);
+  float gsc[NJ], gof[NJ], gsc16[NJ], gof16[NJ];
+  auto set_s = [&](int kt, const uint32_t (&sw)[NJ], const uint32_t (&zw)[NJ]) {
+    const bool hi = ((odd + (lr & p.ngroups) + (kt >> p.gshift)) & 1) != 0;
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+      gsc[j] = p.plain_codes ? 1.f : __uint_as_float(hi ? (sw[j] & 0xFFFF0000u) : (sw[j] << 16));
+      if constexpr (MX) {
+        gsc16[j] = gsc[j] * 0.0625f;
+        gof[j] = zm0 * gsc[j];
+        gof16[j] = zm1 * gsc[j];
+      } else {
+        const float z = Z ? __uint_as_float(hi ? (zw[j] & 0xFFFF0000u) : (zw[j] << 16)) : p.zero_const;
+        gof[j] = -z * gsc[j];
+      }
+    }
+  };
+  auto read_a = [&](int kt, int ks, bf16x8 (&af)[MI]) {
+    const uint8_t* st = smem + (kt % RING) * STAGE;
+#pragma unroll
+    for (int i = 0; i < MI; ++i)
+      af[i] = *reinterpret_cast<const bf16x8*>(st + (i * 32 + lr) * 128 + (((lh * 4 + ks) ^ a_sw) << 4));
+  };
+  auto dq = [&](const uint4 (&bw)[NJ], int ks, bf16x8 (&bfr)[NJ]) {
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+      const uint32_t w = ks == 0 ? bw[j].x : ks == 1 ? bw[j].y : ks == 2 ? bw[j].z : bw[j].w;
+      bfr[j] = MX ? unpack8_scaled_mix(w, gsc[j], gsc16[j], gof[j], gof16[j], magic_v)
+                  : unpack8_scaled(w, gsc[j], gof[j]);
+    }
+  };
+  // the MFMAs of one slice, with the unpacking of the next spread among them
+  constexpr int VPM = ((MX ? 40 : 52) + MI * NJ - 1) / (MI * NJ);
+  auto mm = [&](const bf16x8 (&af)[MI], const bf16x8 (&bfr)[NJ]) {
+#pragma unroll
+    for (int i = 0; i < MI; ++i)
+#pragma unroll
+      for (int j = 0; j < NJ; ++j)
+        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(af[i], bfr[j], acc[i][j], 0, 0, 0);
+#pragma unroll
+    for (int q = 0; q < MI * NJ; ++q) {
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);    // one MFMA
+      __builtin_amdgcn_sched_group_barrier(0x002, VPM, 0);  // VALU
+      if (q < MI) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);  // one LDS read
+    }
+  };
+
+  // ---- main loop.  The barrier in step t publishes stage t + 1 (its loads
+  // landed: at most step t + 2's are in flight) and frees stage t (every wave
+  // holds its last operands in registers), into which step t + 3 then goes.
+  asm volatile("s_nop 4");  // VALU-written SGPRs (descriptors) read by the first loads
+  issue_part(0, 0, LOADS);
+  issue_part(1, 0, LOADS);
+  wait_vmcnt<LOADS>();
+  __syncthreads();
+  issue_fenced(2, 0, P1);
+  uint4 bw[NJ];
+  uint32_t sw[NJ], zw[NJ];
+  bf16x8 a0[MI], a1[MI], b0[NJ], b1[NJ];
+  read_b(0, bw);
+  read_s(0, sw, zw);
+  set_s(0, sw, zw);
+  read_a(0, 0, a0);
+  dq(bw, 0, b0);
+  for (int kt = 0; kt < nk; ++kt) {
+    read_a(kt, 1, a1);
+    dq(bw, 1, b1);
+    mm(a0, b0);
+    issue_fenced(kt + 2, P1, P2);
+    read_a(kt, 2, a0);
+    dq(bw, 2, b0);
+    mm(a1, b1);
+    issue_fenced(kt + 2, P2, LOADS);
+    read_a(kt, 3, a1);
+    dq(bw, 3, b1);
+    mm(a0, b0);
+    wait_vmcnt<LOADS>();
+    __syncthreads();
+    issue_fenced(kt + 3, 0, P1);
+    read_b(kt + 1, bw);
+    read_s(kt + 1, sw, zw);
+    read_a(kt + 1, 0, a0);
+    set_s(kt + 1, sw, zw);
+    dq(bw, 0, b0);
+    mm(a1, b1);
+  }
+  wait_vmcnt<0>();  // no load may still be writing LDS below
+  __syncthreads();
+
+  // ---- epilogue: round to bf16, stage rows in LDS, store 16 bytes a lane.
+  // Element e of lane l: row 8 (e / 4) + 4 (l / 32) + e % 4, column l % 32.
+  float sc[NJ];
+#pragma unroll
+  for (int j = 0; j < NJ; ++j) {
+    const int col = col0 + j * 32 + lr;
+    sc[j] = p.plain_codes && col < rows_b ? bf16_to_f32(p.scales[en0 + col]) : 1.f;
+  }
+  static_assert(BM * TC_PITCH <= RING * STAGE, "staged rows fit the ring");
+  const bool vec_ok = (p.n & 7) == 0;  // rows of C 16-byte aligned
+#pragma unroll
+  for (int i = 0; i < MI; ++i)
+#pragma unroll
+    for (int j = 0; j < NJ; ++j)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const int srow = i * 32 + 8 * (e / 4) + 4 * lh + (e % 4);
+        *reinterpret_cast<uint16_t*>(smem + srow * TC_PITCH + (col0 + j * 32 + lr) * 2) =
+            __builtin_bit_cast(uint16_t, (__bf16)(acc[i][j][e] * sc[j]));
+      }
+  __syncthreads();
+  for (int q = tid; q < t.rows * 32; q += 256) {
+    const int row = q >> 5, cch = q & 31;
+    const int64_t col = n0 + cch * 8;
+    if (col >= p.n) continue;
+    const uint4 v = *reinterpret_cast<const uint4*>(smem + row * TC_PITCH + cch * 16);
+    uint16_t* dst = p.c + (int64_t)(t.row0 + row) * p.n + col;
+    if (vec_ok) {
+      *reinterpret_cast<uint4*>(dst) = v;
+    } else {
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+      for (int u = 0; u < 8 && col + u < p.n; ++u) dst[u] = (uint16_t)(w[u / 2] >> (16 * (u % 2)));
+    }
+  }
+}
+
+template <int MI>
+hipError_t launch_tile(EArgs p, hipStream_t s) {
+  constexpr int SHIFT = MI == 4 ? 7 : 6;
+  p.tiles_n = (int)((p.n + TN - 1) / TN);
+  const dim3 grid((unsigned)(row_tiles_bound(p.slots, p.experts, SHIFT) * p.tiles_n)), wg(256);
+  // the fp16-magic unpacking needs a zero that is a multiple of 2^-5 below 1024
+  const float zs = p.zero_const * 32.f;
+  const bool mix = std::fabs(p.zero_const) < 1024.f && zs == std::nearbyint(zs);
+  if (p.zeros) hipLaunchKernelGGL((k_experts_tile<MI, true, false>), grid, wg, 0, s, p);
+  else if (mix) hipLaunchKernelGGL((k_experts_tile<MI, false, true>), grid, wg, 0, s, p);
+  else hipLaunchKernelGGL((k_experts_tile<MI, false, false>), grid, wg, 0, s, p);
   return hipGetLastError();
 }
 
@@ -189,13 +543,29 @@ hipError_t launch_gemm_w4a16_experts(const uint16_t* a, int64_t a_rows, const in
   p.slots = (int)slots;
   p.experts = (int)experts;
   p.ngroups = (int)(k / group);
-  // 128-k chunks, or 64-k ones where a group or k is no multiple of 128
+  // tiles from 16 rows an expert on (64 experts, k = 4096, n = 2816: 151 us
+  // against 128 with few rows a tile at 16, 168 against 200 at 32)
+  const int64_t mean = slots / experts;
+  if (mean >= 20) {
+    p.gshift = 0;
+    while ((int64_t(64) << p.gshift) < group) ++p.gshift;
+    // q - z is exact in bf16's 8 bits for a multiple of 1/8 within 16
+    p.plain_codes = group == k && !zeros && std::fabs(zero_const) <= 16.f &&
+                    zero_const * 8.f == std::nearbyint(zero_const * 8.f);
+    if (mean >= 96) return launch_tile<4>(p, s);
+    return launch_tile<2>(p, s);
+  }
+  // 128-k chunks, or 64-k ones where a group or k is no multiple of 128.  Two
+  // column blocks a wave (which share the LDS reads of A) where that leaves four
+  // workgroups a CU: 97 us against 107 with one block at 512 rows of 64 experts
+  // (k = 4096, n = 2816), but 15.2 against 14.1 at 8 rows.
+  const bool wide = row_tiles_bound(slots, experts, FEW_SHIFT) * (n / 128) >= 1024;
   if (group % 128 == 0) {
     p.group_chunks = (int)(group / 128);
-    return launch_rows16<1, 4>(p, s);
+    return wide ? launch_few<2, 4>(p, s) : launch_few<1, 4>(p, s);
   }
   p.group_chunks = (int)(group / 64);
-  return launch_rows16<1, 2>(p, s);
+  return wide ? launch_few<2, 2>(p, s) : launch_few<1, 2>(p, s);
 }
 
 }  // namespace wq

@@ -12,6 +12,19 @@ struct RowTile {
   int rows;   // rows in the tile, at least 1
 };
 
+// Inclusive sum over the wave's lanes, in the vector units' own lane moves (row
+// shifts by 1, 2, 4, 8, then the last lanes of rows 0, 2 and of the lower half
+// to the rows after them): no LDS round trip.
+__device__ __forceinline__ int wave_scan(int x) {
+  x += __builtin_amdgcn_update_dpp(0, x, 0x111, 0xF, 0xF, false);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x112, 0xF, 0xF, false);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x114, 0xF, 0xF, false);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x118, 0xF, 0xF, false);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x142, 0xA, 0xF, false);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x143, 0xC, 0xF, false);
+  return x;
+}
+
 // Tile m of the sorted rows (bins 0 .. bins - 1, and with TAIL the rows behind
 // them up to `slots` as one more).  Called by whole waves: every lane takes
 // one bin of 64 at a time, a wave scan numbers the tiles.  Offsets are clamped
@@ -32,12 +45,7 @@ __device__ __forceinline__ bool find_row_tile(const int* __restrict__ offsets, i
       hi = TAIL && b == bins ? slots : min(max(offsets[b + 1], lo), slots);
     }
     const int tiles = (hi - lo + (1 << shift) - 1) >> shift;
-    int incl = tiles;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      const int v = __shfl_up(incl, d);
-      incl += lane >= d ? v : 0;
-    }
+    const int incl = wave_scan(tiles);
     const int sum = __builtin_amdgcn_readlane(incl, 63);
     if (!found && m < run + sum) {
       const int l = __ffsll((unsigned long long)__ballot(incl > m - run)) - 1;
@@ -52,6 +60,19 @@ __device__ __forceinline__ bool find_row_tile(const int* __restrict__ offsets, i
   }
   count = run;
   return found;
+}
+
+// The number of row tiles alone (whole waves, as above).
+__device__ __forceinline__ int count_row_tiles(const int* __restrict__ offsets, int bins, int slots, int shift) {
+  const int lane = threadIdx.x & 63;
+  int tiles = 0;
+  for (int b = lane; b < bins; b += 64) {
+    const int lo = min(max(offsets[b], 0), slots), hi = min(max(offsets[b + 1], lo), slots);
+    tiles += (hi - lo + (1 << shift) - 1) >> shift;
+  }
+#pragma unroll
+  for (int d = 32; d > 0; d >>= 1) tiles += __shfl_xor(tiles, d);
+  return __builtin_amdgcn_readfirstlane(tiles);
 }
 
 }  // namespace wq

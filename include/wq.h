@@ -431,11 +431,10 @@ int wq_combine_rows_grad(const void* d_out, const void* rows, int dtype, const i
  *           they were.
  * One row or many: the kernel is chosen from slots, experts, n and k alone, and
  * reads only the weights of experts that have rows.  Accumulates in float32.
- * Finite a, scales and zeros are assumed.  Where many rows share an
- * expert each weight is first rounded to bf16((q - z) * s) as in
- * wq_gemm_w4a16; with few rows, and with one scale per column, no weight is
- * rounded (one scale per column: if q - z is exact in bf16, as it is for
- * integer zeros).
+ * Finite a, scales and zeros are assumed.  With few rows an expert no weight
+ * is rounded; where many share one each weight is first rounded to
+ * bf16((q - z) * s) as in wq_gemm_w4a16, except with one scale per column and
+ * a zero_const that is a multiple of 1/8 within 16 (then q - z is exact).
  * Bitwise repeatable.  Requires k % 64 == 0, k <= 2^22, slots <= 2^24,
  * 1 <= experts <= 1024, n * experts < 2^31, a gathered `a` below 2 GiB;
  * a, b and c_out 16-byte aligned, scales and zeros 4-byte (whole aligned
