@@ -231,8 +231,9 @@ hipError_t launch_few(EArgs p, hipStream_t s) {
 // ------------------------------------------------------- tiles of many rows
 //
 // Bound by the matrix cores where an expert has hundreds of rows, by its
-// weights' bytes where it has tens.  A workgroup computes 32 MI rows x 256
-// columns, each of its four waves all rows x 64 columns (MI x 2 blocks of
+// weights' bytes and their unpacking where it has tens.  A workgroup computes
+// 32 MI rows x 256 columns, MI up to 4, each of its four waves all rows x 64
+// columns (MI x 2 blocks of
 // v_mfma_f32_32x32x16_bf16), so every packed word is unpacked by one wave.  k
 // advances 64 a step through a three-stage LDS ring that buffer loads fill
 // directly: A's rows (gathered by per-lane offsets), B packed, and the 4-byte
@@ -242,47 +243,27 @@ hipError_t launch_few(EArgs p, hipStream_t s) {
 // is unpacked; with one scale per column and a constant zero that leaves q - z
 // exact in bf16 it stays q - z and the scale goes on the sum.
 //
-// MI = 4 keeps two workgroups on a CU (75 KiB of LDS and 256 registers each):
-// one multiplies while the other waits at its barrier or starts its tile.
+// Two workgroups share a CU (75 KiB of LDS and 256 registers a lane each): one
+// multiplies while the other waits at its barrier or starts its tile.  (256-row
+// tiles, one workgroup a CU: 831 us against 795 for a prompt of 4096 tokens, top
+// 8 of 64 experts, k = 4096, n = 2816; 64-row tiles, three a CU: 990.)
 constexpr int TN = 256, TK = 64, RING = 3;
 constexpr int TB_BYTES = TN * TK / 2, TS_BYTES = TN * 4;
 
 template <int MI, bool Z> constexpr int tile_stage() { return MI * 32 * TK * 2 + TB_BYTES + TS_BYTES * (Z ? 2 : 1); }
 template <int MI, bool Z> constexpr int tile_loads() { return MI + 2 + (Z ? 2 : 1); }
-// workgroups a CU holds by LDS
-template <int MI> constexpr int tile_wgs() { return MI == 4 ? 2 : 3; }
+constexpr int TILE_SHIFT = 7, TILE_BLOCKS = 4;  // a full tile: 128 rows
 constexpr int TC_PITCH = TN * 2 + 16;  // staged C row: rows 4 apart fall in different banks
 
 // A-tile swizzle: physical 16-byte column of k-chunk c in row r is c ^ tile_swz(r)
 __device__ __forceinline__ int tile_swz(int r) { return (r & 7) ^ ((r >> 3) & 1); }
 
+// One tile of up to 32 MI rows (t) and columns tn TN ..
 template <int MI, bool Z, bool MX>
-__global__ __launch_bounds__(256, tile_wgs<MI>()) void k_experts_tile(EArgs p) {
+__device__ __forceinline__ void experts_tile(const EArgs& p, const RowTile& t, int tn, uint8_t* smem) {
   static_assert(!(Z && MX), "the fp16-magic unpacking serves a constant zero");
   constexpr int BM = 32 * MI, NJ = 2;
   constexpr int A_BYTES = BM * TK * 2, STAGE = tile_stage<MI, Z>(), LOADS = tile_loads<MI, Z>();
-  constexpr int SHIFT = MI == 4 ? 7 : 6;
-  __shared__ __attribute__((aligned(1024))) uint8_t smem[RING * STAGE];
-
-  // ---- which tile: the workgroups that have one are numbered so that each XCD
-  // (8, dispatched round-robin) gets a compact run of them, bands of 8 row
-  // tiles by all columns, and shares A and B rows in its own L2
-  const int tiles_m = count_row_tiles(p.offsets, p.experts, p.slots, SHIFT);
-  const int nwg = tiles_m * p.tiles_n;
-  int id = blockIdx.x;
-  if (id >= nwg) return;
-  {
-    const int xcd = id & 7, each = nwg >> 3, rest = nwg & 7;
-    id = xcd * each + min(xcd, rest) + (id >> 3);
-  }
-  const int per_band = 8 * p.tiles_n;
-  const int first_m = id / per_band * 8, in_band = id % per_band;
-  const int band_rows = min(8, tiles_m - first_m);
-  const int tn = in_band / band_rows;
-  RowTile t;
-  int count;
-  if (!find_row_tile<false>(p.offsets, p.experts, p.slots, SHIFT, first_m + in_band % band_rows, t, count)) return;
-
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int col0 = wave * 64;
@@ -507,17 +488,44 @@ __global__ __launch_bounds__(256, tile_wgs<MI>()) void k_experts_tile(EArgs p) {
   }
 }
 
-template <int MI>
-hipError_t launch_tile(EArgs p, hipStream_t s) {
-  constexpr int SHIFT = MI == 4 ? 7 : 6;
+// An expert's last tile takes the body of as many blocks as it has rows (prompt
+// of 4096 tokens, 64 experts, top 8: 795 -> 781 us; 256 tokens: 203 -> 157).
+template <bool Z, bool MX>
+__global__ __launch_bounds__(256, 2) void k_experts_tiles(EArgs p) {
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[RING * tile_stage<TILE_BLOCKS, Z>()];
+  // the workgroups that have a tile are numbered so that each XCD (8, dispatched
+  // round-robin) gets a compact run of them, bands of 8 row tiles by all
+  // columns, and shares A and B rows in its own L2
+  const int tiles_m = count_row_tiles(p.offsets, p.experts, p.slots, TILE_SHIFT);
+  const int nwg = tiles_m * p.tiles_n;
+  int id = blockIdx.x;
+  if (id >= nwg) return;
+  {
+    const int xcd = id & 7, each = nwg >> 3, rest = nwg & 7;
+    id = xcd * each + min(xcd, rest) + (id >> 3);
+  }
+  const int per_band = 8 * p.tiles_n;
+  const int first_m = id / per_band * 8, in_band = id % per_band;
+  const int band_rows = min(8, tiles_m - first_m);
+  const int tn = in_band / band_rows;
+  RowTile t;
+  int count;
+  if (!find_row_tile<false>(p.offsets, p.experts, p.slots, TILE_SHIFT, first_m + in_band % band_rows, t, count)) return;
+  if (t.rows <= 32) experts_tile<1, Z, MX>(p, t, tn, smem);
+  else if (t.rows <= 64) experts_tile<2, Z, MX>(p, t, tn, smem);
+  else if (t.rows <= 96) experts_tile<3, Z, MX>(p, t, tn, smem);
+  else experts_tile<TILE_BLOCKS, Z, MX>(p, t, tn, smem);
+}
+
+hipError_t launch_tiles(EArgs p, hipStream_t s) {
   p.tiles_n = (int)((p.n + TN - 1) / TN);
-  const dim3 grid((unsigned)(row_tiles_bound(p.slots, p.experts, SHIFT) * p.tiles_n)), wg(256);
+  const dim3 grid((unsigned)(row_tiles_bound(p.slots, p.experts, TILE_SHIFT) * p.tiles_n)), wg(256);
   // the fp16-magic unpacking needs a zero that is a multiple of 2^-5 below 1024
   const float zs = p.zero_const * 32.f;
   const bool mix = std::fabs(p.zero_const) < 1024.f && zs == std::nearbyint(zs);
-  if (p.zeros) hipLaunchKernelGGL((k_experts_tile<MI, true, false>), grid, wg, 0, s, p);
-  else if (mix) hipLaunchKernelGGL((k_experts_tile<MI, false, true>), grid, wg, 0, s, p);
-  else hipLaunchKernelGGL((k_experts_tile<MI, false, false>), grid, wg, 0, s, p);
+  if (p.zeros) hipLaunchKernelGGL((k_experts_tiles<true, false>), grid, wg, 0, s, p);
+  else if (mix) hipLaunchKernelGGL((k_experts_tiles<false, true>), grid, wg, 0, s, p);
+  else hipLaunchKernelGGL((k_experts_tiles<false, false>), grid, wg, 0, s, p);
   return hipGetLastError();
 }
 
@@ -543,8 +551,8 @@ hipError_t launch_gemm_w4a16_experts(const uint16_t* a, int64_t a_rows, const in
   p.slots = (int)slots;
   p.experts = (int)experts;
   p.ngroups = (int)(k / group);
-  // tiles from 16 rows an expert on (64 experts, k = 4096, n = 2816: 151 us
-  // against 128 with few rows a tile at 16, 168 against 200 at 32)
+  // tiles from 20 rows an expert on (64 experts, k = 4096, n = 2816: 136 us
+  // against 126 with few rows a tile at 16 rows, 157 against 200 at 32)
   const int64_t mean = slots / experts;
   if (mean >= 20) {
     p.gshift = 0;
@@ -552,8 +560,7 @@ hipError_t launch_gemm_w4a16_experts(const uint16_t* a, int64_t a_rows, const in
     // q - z is exact in bf16's 8 bits for a multiple of 1/8 within 16
     p.plain_codes = group == k && !zeros && std::fabs(zero_const) <= 16.f &&
                     zero_const * 8.f == std::nearbyint(zero_const * 8.f);
-    if (mean >= 96) return launch_tile<4>(p, s);
-    return launch_tile<2>(p, s);
+    return launch_tiles(p, s);
   }
   // 128-k chunks, or 64-k ones where a group or k is no multiple of 128.  Two
   // column blocks a wave (which share the LDS reads of A) where that leaves four
