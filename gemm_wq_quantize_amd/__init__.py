@@ -345,19 +345,43 @@ def _gemv_ternary_ptq1_1(name, superblocks, codebook, esc_idx, esc_patt, x_q8, k
 _ROW_DTYPES = (torch.float32, torch.float16, torch.bfloat16)
 
 
-def _call(name, st, *args):
-    """The C function on stream ``st``, with the stream's device current."""
+def _where(stream):
+    """(device index, hipStream_t) of ``stream``, or of torch's current stream
+    (its handle alone: building a Stream object takes 2.6 us, as long as a launch)."""
+    if stream is None:
+        dev = torch.cuda.current_device()
+        return dev, torch._C._cuda_getCurrentRawStream(dev)
+    return stream.device_index, stream.cuda_stream
+
+
+def _at(t, dev):
+    """The address of a contiguous tensor on device ``dev`` (None stays None)."""
+    if t is None:
+        return None
+    if not t.is_cuda:
+        raise ValueError("wq: tensors must be on the GPU")
+    if not t.is_contiguous():
+        raise ValueError("wq: tensors must be contiguous")
+    if t.get_device() != dev:
+        raise ValueError(f"wq: tensor on {t.device}, stream on cuda:{dev}")
+    return t.data_ptr()
+
+
+def _call(name, dev, raw, *args):
+    """The C function on stream ``raw``, with its device current."""
     fn = getattr(load_library(), name)
-    if st.device_index == torch.cuda.current_device():
-        _check(name, fn(*args, st.cuda_stream))
+    if dev == torch.cuda.current_device():
+        status = fn(*args, raw)
     else:
-        with torch.cuda.device(st.device_index):
-            _check(name, fn(*args, st.cuda_stream))
+        with torch.cuda.device(dev):
+            status = fn(*args, raw)
+    if status != WQ_OK:
+        raise WqError(name, status)
 
 
-def _workspace(name, st, workspace, need):
+def _workspace(name, stream, workspace, need):
     """The caller's workspace (any dtype), or one from torch's allocator that
-    is reused in the order of stream ``st`` alone."""
+    is reused in the order of the call's stream alone."""
     if need < 0:
         raise WqError(name, need)
     if workspace is not None:
@@ -366,8 +390,10 @@ def _workspace(name, st, workspace, need):
         return workspace, nbytes
     if need == 0:
         return None, 0
-    with torch.cuda.stream(st):
-        return torch.empty(need, dtype=torch.uint8, device=st.device), need
+    if stream is None:
+        return torch.empty(need, dtype=torch.uint8, device="cuda"), need
+    with torch.cuda.stream(stream):
+        return torch.empty(need, dtype=torch.uint8, device=stream.device), need
 
 
 def _plan_i32(*tensors):
@@ -392,11 +418,10 @@ def wq_sort_rows(ids, bins, offsets, order, place, workspace=None, stream=None):
     _plan_i32(ids, offsets, order, place)
     _require(offsets.numel() == bins + 1, "offsets hold bins + 1 values")
     _require(order.numel() == t * topk and place.numel() == t * topk, "order and place hold t * topk values")
-    st = _stream(stream)
-    d = st.device
-    args = (_ptr(ids, d), t, topk, bins, _ptr(offsets, d), _ptr(order, d), _ptr(place, d))
-    ws, nbytes = _workspace("wq_sort_rows", st, workspace, lib.wq_sort_rows_workspace(t, topk, bins))
-    _call("wq_sort_rows", st, *args, _ptr(ws, d), nbytes)
+    d, raw = _where(stream)
+    args = (_at(ids, d), t, topk, bins, _at(offsets, d), _at(order, d), _at(place, d))
+    ws, nbytes = _workspace("wq_sort_rows", stream, workspace, lib.wq_sort_rows_workspace(t, topk, bins))
+    _call("wq_sort_rows", d, raw, *args, _at(ws, d), nbytes)
 
 
 def _moved(x, place, rows):
@@ -414,9 +439,8 @@ def _moved(x, place, rows):
 def wq_dispatch_rows(x, place, out, stream=None):
     """out[place[i][j]] = x[i]: x [t][h] (f32, f16 or bf16) to out [t * topk][h]."""
     t, topk, h = _moved(x, place, out)
-    st = _stream(stream)
-    d = st.device
-    _call("wq_dispatch_rows", st, _ptr(x, d), _dtype(x, _ROW_DTYPES), _ptr(place, d), t, topk, h, _ptr(out, d))
+    d, raw = _where(stream)
+    _call("wq_dispatch_rows", d, raw, _at(x, d), _dtype(x, _ROW_DTYPES), _at(place, d), t, topk, h, _at(out, d))
 
 
 def _row_weights(weights, place):
@@ -429,10 +453,9 @@ def wq_combine_rows(rows, place, weights, out, stream=None):
     t, topk, h = _moved(out, place, rows)
     if weights is not None:
         _row_weights(weights, place)
-    st = _stream(stream)
-    d = st.device
-    _call("wq_combine_rows", st, _ptr(rows, d), _dtype(rows, _ROW_DTYPES), _ptr(place, d), _ptr(weights, d), t, topk, h,
-          _ptr(out, d))
+    d, raw = _where(stream)
+    _call("wq_combine_rows", d, raw, _at(rows, d), _dtype(rows, _ROW_DTYPES), _at(place, d), _at(weights, d), t, topk, h,
+          _at(out, d))
 
 
 def wq_combine_rows_grad(d_out, rows, place, weights, d_rows, d_weights, stream=None):
@@ -442,10 +465,9 @@ def wq_combine_rows_grad(d_out, rows, place, weights, d_rows, d_weights, stream=
     _moved(d_out, place, d_rows)
     _row_weights(weights, place)
     _row_weights(d_weights, place)
-    st = _stream(stream)
-    d = st.device
-    _call("wq_combine_rows_grad", st, _ptr(d_out, d), _ptr(rows, d), _dtype(rows, _ROW_DTYPES), _ptr(place, d),
-          _ptr(weights, d), t, topk, h, _ptr(d_rows, d), _ptr(d_weights, d))
+    d, raw = _where(stream)
+    _call("wq_combine_rows_grad", d, raw, _at(d_out, d), _at(rows, d), _dtype(rows, _ROW_DTYPES), _at(place, d),
+          _at(weights, d), t, topk, h, _at(d_rows, d), _at(d_weights, d))
 
 
 def wq_gemm_w4a16_experts(a, order, topk, offsets, b, layout, scales, zeros, group, zero_const, c_out, stream=None):
@@ -472,10 +494,9 @@ def wq_gemm_w4a16_experts(a, order, topk, offsets, b, layout, scales, zeros, gro
                  "with order, a is [slots / topk][k] and order [slots]")
     else:
         _require(a_rows == slots, "without order, a is [slots][k]")
-    st = _stream(stream)
-    d = st.device
-    _call("wq_gemm_w4a16_experts", st, _ptr(a, d), a_rows, _ptr(order, d), topk, _ptr(offsets, d), slots, e,
-          _ptr(b, d), layout, _ptr(scales, d), _ptr(zeros, d), group, float(zero_const), n, k, _ptr(c_out, d))
+    d, raw = _where(stream)
+    _call("wq_gemm_w4a16_experts", d, raw, _at(a, d), a_rows, _at(order, d), topk, _at(offsets, d), slots, e,
+          _at(b, d), layout, _at(scales, d), _at(zeros, d), group, float(zero_const), n, k, _at(c_out, d))
 
 
 def wq_lora_workspace(t, k, adapters, rank):
@@ -504,12 +525,11 @@ def wq_lora(x, order, offsets, a, b, scales, base, out, workspace=None, stream=N
     _require(scales.dtype == torch.float32 and scales.numel() == n_ad, "scales are fp32, one an adapter")
     _plan_i32(order, offsets)
     _require(order.numel() == t and offsets.numel() == n_ad + 1, "order holds t values, offsets adapters + 1")
-    st = _stream(stream)
-    d = st.device
-    args = (_ptr(x, d), t, k, _ptr(order, d), _ptr(offsets, d), n_ad, _ptr(a, d), _ptr(b, d), rank, _ptr(scales, d),
-            _ptr(base, d), _ptr(out, d), _dtype(out), n)
-    ws, nbytes = _workspace("wq_lora", st, workspace, lib.wq_lora_workspace(t, k, n_ad, rank))
-    _call("wq_lora", st, *args, _ptr(ws, d), nbytes)
+    d, raw = _where(stream)
+    args = (_at(x, d), t, k, _at(order, d), _at(offsets, d), n_ad, _at(a, d), _at(b, d), rank, _at(scales, d),
+            _at(base, d), _at(out, d), _dtype(out), n)
+    ws, nbytes = _workspace("wq_lora", stream, workspace, lib.wq_lora_workspace(t, k, n_ad, rank))
+    _call("wq_lora", d, raw, *args, _at(ws, d), nbytes)
 
 
 # ---- calibration kernels (include/wq_peaks.h): practical ceilings of the
