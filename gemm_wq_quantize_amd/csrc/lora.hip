@@ -41,11 +41,15 @@ __device__ __forceinline__ int64_t x_row(const LArgs& p, int i) {
 // ------------------------------------------------------------ v = A x
 //
 // A workgroup takes MB blocks of 16 rows, NR blocks of 16 ranks and one part of
-// k; its four waves take every fourth 32-k chunk and join in LDS.  Operands
-// go from memory to v_mfma_f32_16x16x32_bf16 as they lie: 16 bytes of a row
-// are a lane's 8 slots.  Rows and ranks past the last repeat it.
+// k; its four waves take a quarter of that each and join in LDS.  Operands go
+// from memory to v_mfma_f32_16x16x32_bf16 as they lie, DEPTH 32-k chunks ahead:
+// 16 bytes of a row are a lane's 8 slots.  Rows and ranks past the last repeat
+// it.
+template <int MB> constexpr int tile_shift() { return MB == 1 ? 4 : MB == 2 ? 5 : 6; }
+
 template <int MB, int NR>
 __global__ __launch_bounds__(256) void k_lora_shrink(LArgs p) {
+  constexpr int DEPTH = MB + NR <= 3 ? 8 : MB + NR <= 6 ? 4 : 2;
   __shared__ __attribute__((aligned(16))) float part[4][MB * NR * 4][64];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -55,39 +59,56 @@ __global__ __launch_bounds__(256) void k_lora_shrink(LArgs p) {
   const int part_k = (int)(id % (unsigned)p.parts), m = (int)(id / (unsigned)p.parts);
   RowTile t;
   int count;
-  constexpr int SHIFT = MB == 1 ? 4 : 6;
-  static_assert(MB == 1 || MB == 4, "tiles of 16 or 64 rows");
-  if (!find_row_tile<false>(p.offsets, p.adapters, p.t, SHIFT, m, t, count)) return;
+  if (!find_row_tile<false>(p.offsets, p.adapters, p.t, tile_shift<MB>(), m, t, count)) return;
 
   const int lr = lane & 15, lq = lane >> 4;
+  const int nch = (int)(p.k / 32);
+  // this wave's chunks: the parts' waves in the order of k
+  const int slot = part_k * 4 + wave, slots = p.parts * 4;
+  const int c0 = (int)((int64_t)nch * slot / slots), cnt = (int)((int64_t)nch * (slot + 1) / slots) - c0;
   const uint16_t* xr[MB];
   const uint16_t* ar[NR];
 #pragma unroll
-  for (int i = 0; i < MB; ++i)
-    xr[i] = p.x + max(x_row(p, t.row0 + min(i * 16 + lr, t.rows - 1)), (int64_t)0) * p.k + lq * 8;
-#pragma unroll
   for (int j = 0; j < NR; ++j)
-    ar[j] = p.a + ((int64_t)t.bin * p.rank + min(rg * (NR * 16) + j * 16 + lr, p.rank - 1)) * p.k + lq * 8;
+    ar[j] = p.a + ((int64_t)t.bin * p.rank + min(rg * (NR * 16) + j * 16 + lr, p.rank - 1)) * p.k + c0 * 32 + lq * 8;
+#pragma unroll
+  for (int i = 0; i < MB; ++i)
+    xr[i] = p.x + max(x_row(p, t.row0 + min(i * 16 + lr, t.rows - 1)), (int64_t)0) * p.k + c0 * 32 + lq * 8;
   floatx4 acc[MB][NR];
 #pragma unroll
   for (int i = 0; i < MB; ++i)
 #pragma unroll
     for (int j = 0; j < NR; ++j) acc[i][j] = floatx4{0.f, 0.f, 0.f, 0.f};
-  const int nch = (int)(p.k / 32);
-  const int c0 = (int)((int64_t)nch * part_k / p.parts), c1 = (int)((int64_t)nch * (part_k + 1) / p.parts);
-#pragma unroll 4
-  for (int ch = c0 + wave; ch < c1; ch += 4) {
-    bf16x8 xf[MB], af[NR];
+  bf16x8 xf[DEPTH][MB], af[DEPTH][NR];
+  auto load = [&](int ch, int d) {
 #pragma unroll
-    for (int i = 0; i < MB; ++i) xf[i] = *reinterpret_cast<const bf16x8*>(xr[i] + (int64_t)ch * 32);
+    for (int j = 0; j < NR; ++j) af[d][j] = *reinterpret_cast<const bf16x8*>(ar[j] + (int64_t)ch * 32);
 #pragma unroll
-    for (int j = 0; j < NR; ++j) af[j] = *reinterpret_cast<const bf16x8*>(ar[j] + (int64_t)ch * 32);
+    for (int i = 0; i < MB; ++i) xf[d][i] = *reinterpret_cast<const bf16x8*>(xr[i] + (int64_t)ch * 32);
+  };
+  auto fold = [&](int d) {
 #pragma unroll
     for (int i = 0; i < MB; ++i)
 #pragma unroll
       for (int j = 0; j < NR; ++j)
-        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf[i], af[j], acc[i][j], 0, 0, 0);
-  }
+        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf[d][i], af[d][j], acc[i][j], 0, 0, 0);
+  };
+#pragma unroll
+  for (int d = 0; d < DEPTH; ++d)
+    if (d < cnt) load(d, d);
+  int ch = 0;
+  for (; ch + 2 * DEPTH <= cnt; ch += DEPTH)
+#pragma unroll
+    for (int d = 0; d < DEPTH; ++d) {
+      fold(d);
+      load(ch + d + DEPTH, d);
+    }
+  for (; ch < cnt; ch += DEPTH)
+#pragma unroll
+    for (int d = 0; d < DEPTH; ++d) {
+      if (ch + d < cnt) fold(d);
+      if (ch + d + DEPTH < cnt) load(ch + d + DEPTH, d);
+    }
 #pragma unroll
   for (int i = 0; i < MB; ++i)
 #pragma unroll
@@ -124,109 +145,184 @@ template <typename T> struct Eight;
 template <> struct Eight<__bf16> { struct alignas(2) raw { uint16_t h[8]; }; };
 template <> struct Eight<float> { struct alignas(4) raw { float f[8]; }; };
 
+// ring depth: 64 registers of operands or a little more
 template <typename T, int MB, int RS>
+constexpr int expand_depth() {
+  return MB * (int)sizeof(T) / 2 * 4 + (RS < 2 ? 1 : RS) * 8 <= 24 ? 4 : 2;
+}
+
+template <typename T, int MB, int RS, bool STREAM>
 __global__ __launch_bounds__(256) void k_lora_expand(LArgs p) {
   constexpr int NS = v_parts<T>();
   constexpr int RP = RS == 0 ? 16 : RS * 32;       // slots of a part
   constexpr int STEPS = (NS * RP + 31) / 32;
+  constexpr int NB = RS == 0 ? 1 : RS;             // steps with a B operand of their own: the parts share them
   constexpr int PITCH = STEPS * 32 + 8;            // bf16 per LDS row; 16 bytes off a power of two
+  typedef typename Eight<T>::raw raw_t;
   __shared__ __attribute__((aligned(16))) uint16_t vs[MB * 16 * PITCH];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int m = (int)(blockIdx.x / (unsigned)p.tiles_n), tn = (int)(blockIdx.x % (unsigned)p.tiles_n);
   RowTile t;
   int count;
-  constexpr int SHIFT = MB == 1 ? 4 : 6;
-  if (!find_row_tile<true>(p.offsets, p.adapters, p.t, SHIFT, m, t, count)) return;
+  if (!find_row_tile<true>(p.offsets, p.adapters, p.t, tile_shift<MB>(), m, t, count)) return;
   const bool live = t.bin < p.adapters;
   if (!live && p.out == p.base) return;  // nothing to copy
 
+  const int lr = lane & 15, lq = lane >> 4;
+  const uint16_t* bl = p.b + (int64_t)(live ? t.bin : 0) * p.n * p.rank;
+  // a ring of DEPTH 32-column blocks: B's and base's loads of the next ones are in
+  // flight while one is multiplied.  Columns past n and rows past the tile's last
+  // load another one's and store nothing.
+  constexpr int DEPTH = expand_depth<T, MB, RS>();
+  bf16x8 bf[DEPTH][NB][2];
+  raw_t base[DEPTH][MB];
+  const bool with_base = p.base && p.n >= 8;
+  int64_t orow[MB];   // a lane's rows, -1 where there is none
+  const T* brow[MB];  // base of a row that exists
+  auto block_col = [&](int cb) { return ((int64_t)tn * p.col_blocks + cb) * 128 + wave * 32; };
+  auto load_b = [&](int cb, int d) {
+    const int64_t n0 = block_col(cb);
+#pragma unroll
+    for (int s = 0; s < NB; ++s) {
+      const int r = min((s * 32 + lq * 8) % RP, p.rank - 8);  // slots past the rank meet a zero of v
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int64_t col = min(n0 + (lr >> 2) * 8 + h * 4 + (lr & 3), p.n - 1);
+        bf[d][s][h] = *reinterpret_cast<const bf16x8*>(bl + col * p.rank + r);
+      }
+    }
+  };
+  auto load_base = [&](int cb, int d) {
+    const int64_t c0 = min(block_col(cb) + lq * 8, p.n - 8);
+#pragma unroll
+    for (int i = 0; i < MB; ++i) base[d][i] = *reinterpret_cast<const raw_t*>(brow[i] + c0);
+  };
+  // the first blocks' operands are on their way while v is made ready
+  const int blocks = (int)min((int64_t)p.col_blocks, (p.n - block_col(0) + 127) / 128);  // this wave's
+  if (live)
+#pragma unroll
+    for (int d = 0; d < DEPTH; ++d)
+      if (d < blocks) load_b(d, d);
+#pragma unroll
+  for (int i = 0; i < MB; ++i) {
+    const int64_t r = x_row(p, t.row0 + min(i * 16 + lr, t.rows - 1));
+    orow[i] = i * 16 + lr < t.rows ? r : -1;
+    brow[i] = (const T*)p.base + max(r, (int64_t)0) * p.n;
+  }
+  if (with_base)
+#pragma unroll
+    for (int d = 0; d < DEPTH; ++d)
+      if (d < blocks) load_base(d, d);
+
   if (live) {
     const float scale = p.scales[t.bin];
-    for (int q = tid; q < t.rows * (STEPS * 32); q += 256) vs[(q / (STEPS * 32)) * PITCH + q % (STEPS * 32)] = 0;
-    __syncthreads();
-    for (int q = tid; q < t.rows * p.rank; q += 256) {
-      const int row = q / p.rank, r = q % p.rank;
+    // slots that no rank fills are zero
+    if (RP != p.rank || STEPS * 32 != NS * RP) {
+      for (int q = tid; q < t.rows * (STEPS * 4); q += 256)
+        *reinterpret_cast<u32x4*>(vs + q / (STEPS * 4) * PITCH + q % (STEPS * 4) * 8) = u32x4{0, 0, 0, 0};
+      __syncthreads();
+    }
+    const int quads = p.rank / 4;  // 4 ranks a lane
+    for (int q = tid; q < t.rows * quads; q += 256) {
+      const int row = q / quads, r = q % quads * 4;
       const float* src = p.v + (int64_t)(t.row0 + row) * p.rank_pad + r;
-      float sum = 0.f;
-      for (int u = 0; u < p.parts; ++u) sum += src[(int64_t)u * p.t * p.rank_pad];
-      float left = sum * scale;
+      floatx4 sum = *reinterpret_cast<const floatx4*>(src);
+#pragma unroll 4
+      for (int u = 1; u < p.parts; ++u)
+        sum += *reinterpret_cast<const floatx4*>(src + (int64_t)u * p.t * p.rank_pad);
+      sum *= scale;
 #pragma unroll
       for (int s = 0; s < NS; ++s) {
-        const __bf16 h = (__bf16)left;
-        vs[row * PITCH + s * RP + r] = __builtin_bit_cast(uint16_t, h);
-        left -= (float)h;
+        typedef __bf16 b4 __attribute__((ext_vector_type(4)));
+        const b4 h = __builtin_convertvector(sum, b4);
+        *reinterpret_cast<b4*>(vs + row * PITCH + s * RP + r) = h;
+        sum -= __builtin_convertvector(h, floatx4);
       }
     }
     __syncthreads();
   }
-  const int lr = lane & 15, lq = lane >> 4;
-  int64_t orow[MB];
-#pragma unroll
-  for (int i = 0; i < MB; ++i) orow[i] = i * 16 + lr < t.rows ? x_row(p, t.row0 + i * 16 + lr) : -1;
-  const uint16_t* bl = p.b + (int64_t)(live ? t.bin : 0) * p.n * p.rank;
-  for (int cb = 0; cb < p.col_blocks; ++cb) {
-    const int64_t n0 = ((int64_t)tn * p.col_blocks + cb) * 128 + wave * 32;
-    if (n0 >= p.n) break;
+  auto block = [&](int cb, int d) {
     floatx4 acc[MB][2];
 #pragma unroll
     for (int i = 0; i < MB; ++i) acc[i][0] = acc[i][1] = floatx4{0.f, 0.f, 0.f, 0.f};
     if (live) {
 #pragma unroll
-      for (int s = 0; s < STEPS; ++s) {
-        const int slot = s * 32 + lq * 8;
-        const int r = min(slot % RP, p.rank - 8);  // slots past the rank meet a zero of v
-        bf16x8 bf[2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int64_t col = min(n0 + (lr >> 2) * 8 + h * 4 + (lr & 3), p.n - 1);
-          bf[h] = *reinterpret_cast<const bf16x8*>(bl + col * p.rank + r);
-        }
+      for (int s = 0; s < STEPS; ++s)
 #pragma unroll
         for (int i = 0; i < MB; ++i) {
-          const bf16x8 vf = *reinterpret_cast<const bf16x8*>(vs + (i * 16 + lr) * PITCH + slot);
+          const bf16x8 vf = *reinterpret_cast<const bf16x8*>(vs + (i * 16 + lr) * PITCH + s * 32 + lq * 8);
 #pragma unroll
           for (int h = 0; h < 2; ++h)
-            acc[i][h] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bf[h], vf, acc[i][h], 0, 0, 0);
+            acc[i][h] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bf[d][s % NB][h], vf, acc[i][h], 0, 0, 0);
         }
-      }
     }
-    const int64_t c0 = n0 + lq * 8;
-    if (c0 >= p.n) continue;
+    const int64_t c0 = block_col(cb) + lq * 8;
 #pragma unroll
     for (int i = 0; i < MB; ++i) {
-      if (orow[i] < 0) continue;
-      float f[8];
+      T w[8];
+      if (with_base) __builtin_memcpy(w, &base[d][i], sizeof(w));
+      if (live || !with_base) {  // a row without an adapter keeps base's bits
 #pragma unroll
-      for (int e = 0; e < 8; ++e) f[e] = acc[i][e >> 2][e & 3];
-      const T* src = (const T*)p.base + orow[i] * p.n + c0;
-      T* dst = (T*)p.out + orow[i] * p.n + c0;
-      typedef typename Eight<T>::raw raw_t;
-      if (c0 + 8 <= p.n) {
-        T w[8];
-        if (p.base) __builtin_memcpy(w, reinterpret_cast<const raw_t*>(src), sizeof(w));
-        if (live || !p.base) {  // a row without an adapter keeps base's bits
-#pragma unroll
-          for (int e = 0; e < 8; ++e) w[e] = (T)(p.base ? f[e] + (float)w[e] : f[e]);
+        for (int e = 0; e < 8; ++e) {
+          const float f = acc[i][e >> 2][e & 3];
+          w[e] = (T)(with_base ? f + (float)w[e] : f);
         }
-        __builtin_memcpy(reinterpret_cast<raw_t*>(dst), w, sizeof(w));
+      }
+      if (orow[i] < 0 || c0 >= p.n) continue;
+      T* dst = (T*)p.out + orow[i] * p.n + c0;
+      if (c0 + 8 <= p.n) {
+        uint32x4 v[sizeof(w) / 16];
+        __builtin_memcpy(v, w, sizeof(w));
+#pragma unroll
+        for (int q = 0; q < (int)sizeof(w) / 16; ++q) store_16<STREAM>(reinterpret_cast<uint8_t*>(dst) + 16 * q, v[q]);
       } else {
-        for (int e = 0; e < 8; ++e)
-          if (c0 + e < p.n) dst[e] = !p.base ? (T)f[e] : live ? (T)(f[e] + (float)src[e]) : src[e];
+        const T* src = (const T*)p.base + orow[i] * p.n + c0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float f = acc[i][e >> 2][e & 3];
+          if (c0 + e < p.n) dst[e] = !p.base ? (T)f : live ? (T)(f + (float)src[e]) : src[e];
+        }
       }
     }
-  }
+  };
+  int cb = 0;
+  for (; cb + 2 * DEPTH <= blocks; cb += DEPTH)
+#pragma unroll
+    for (int d = 0; d < DEPTH; ++d) {
+      block(cb + d, d);
+      if (live) load_b(cb + d + DEPTH, d);
+      if (with_base) load_base(cb + d + DEPTH, d);
+    }
+  for (; cb < blocks; cb += DEPTH)
+#pragma unroll
+    for (int d = 0; d < DEPTH; ++d) {
+      if (cb + d >= blocks) break;
+      block(cb + d, d);
+      if (cb + d + DEPTH < blocks) {
+        if (live) load_b(cb + d + DEPTH, d);
+        if (with_base) load_base(cb + d + DEPTH, d);
+      }
+    }
 }
 
-// Rows of a tile: 16 with up to 1024 rows, where most tiles hold a request's
-// one or few rows; 64 above.
-int lora_shift(int64_t t) { return t > 1024 ? 6 : 4; }
+// Rows of a tile.  The first launch reads all of an adapter's A for every tile
+// (from L2), the second all of its B: larger tiles where there are rows to fill
+// them.  Whole calls at rank 64, k = n = 5120, ten requests: first launch with
+// 16, 32, 64 rows 18.3, 19.4, 22.0 us at 512 rows, 67.4, 57.9, 57.5 at 4096 and
+// 242, 208, 186 at 16384; second launch with 16, 32 rows 25.6, 28.8 at 1024, 55.1,
+// 55.3 at 4096 (n = 17280: 123, 112) and 224, 201 at 16384.
+int shrink_shift(int64_t t) { return t >= 8192 ? 6 : t >= 1024 ? 5 : 4; }
+int expand_shift(int64_t t) { return t >= 4096 ? 5 : 4; }
 
-// k parts: enough workgroups to fill the card (512) where row tiles alone do
-// not, each part at least 256 k, so that every wave has two chunks or more.
+// k parts: enough workgroups to fill the card where row tiles alone do not, each
+// part at least 256 k, so that every wave has two chunks or more.  More parts
+// are more sums to join: 256 workgroups, 512 with 64-row tiles (512 and 256 at
+// 2048 rows 40.9 and 37.2 us, at 16384 rows 186 and 202).
 int lora_parts(int64_t t, int64_t adapters, int64_t rank, int64_t k) {
-  const int64_t wgs = row_tiles_bound(t, adapters, lora_shift(t)) * ((rank + 63) / 64);
-  int64_t parts = wgs > 0 ? (511 + wgs) / wgs : 1;
+  const int64_t wgs = row_tiles_bound(t, adapters, shrink_shift(t)) * ((rank + 63) / 64);
+  const int64_t want = shrink_shift(t) == 6 ? 512 : 256;
+  int64_t parts = wgs > 0 ? (want - 1 + wgs) / wgs : 1;
   if (parts > k / 256) parts = k / 256;
   if (parts > 16) parts = 16;
   return parts > 1 ? (int)parts : 1;
@@ -239,26 +335,33 @@ hipError_t shrink(LArgs p, hipStream_t s) {
   const int nr = p.rank <= 16 ? 1 : p.rank <= 32 ? 2 : 4;
   p.rank_groups = (p.rank + nr * 16 - 1) / (nr * 16);
   const unsigned grid =
-      (unsigned)(row_tiles_bound(p.t, p.adapters, MB == 1 ? 4 : 6) * p.parts * p.rank_groups);
+      (unsigned)(row_tiles_bound(p.t, p.adapters, tile_shift<MB>()) * p.parts * p.rank_groups);
   if (nr == 1) hipLaunchKernelGGL((k_lora_shrink<MB, 1>), dim3(grid), dim3(256), 0, s, p);
   else if (nr == 2) hipLaunchKernelGGL((k_lora_shrink<MB, 2>), dim3(grid), dim3(256), 0, s, p);
   else hipLaunchKernelGGL((k_lora_shrink<MB, 4>), dim3(grid), dim3(256), 0, s, p);
   return hipGetLastError();
 }
 
-template <typename T, int MB>
-hipError_t expand(LArgs p, hipStream_t s) {
-  const int64_t tiles = row_tiles_bound(p.t, p.adapters + 1, MB == 1 ? 4 : 6);
+template <typename T, int MB, bool STREAM>
+hipError_t expand_as(LArgs p, hipStream_t s) {
+  const int64_t tiles = row_tiles_bound(p.t, p.adapters + 1, tile_shift<MB>());
   const int64_t blocks = (p.n + 127) / 128;
+  // as many columns a workgroup as leave 1024 workgroups: v is made ready once in each
   p.col_blocks = 1;
   while (p.col_blocks < 8 && tiles * (blocks / (2 * p.col_blocks)) >= 1024) p.col_blocks *= 2;
   p.tiles_n = (int)((blocks + p.col_blocks - 1) / p.col_blocks);
   const dim3 grid((unsigned)(tiles * p.tiles_n)), wg(256);
-  if (p.rank <= 16) hipLaunchKernelGGL((k_lora_expand<T, MB, 0>), grid, wg, 0, s, p);
-  else if (p.rank <= 32) hipLaunchKernelGGL((k_lora_expand<T, MB, 1>), grid, wg, 0, s, p);
-  else if (p.rank <= 64) hipLaunchKernelGGL((k_lora_expand<T, MB, 2>), grid, wg, 0, s, p);
-  else hipLaunchKernelGGL((k_lora_expand<T, MB, 4>), grid, wg, 0, s, p);
+  if (p.rank <= 16) hipLaunchKernelGGL((k_lora_expand<T, MB, 0, STREAM>), grid, wg, 0, s, p);
+  else if (p.rank <= 32) hipLaunchKernelGGL((k_lora_expand<T, MB, 1, STREAM>), grid, wg, 0, s, p);
+  else if (p.rank <= 64) hipLaunchKernelGGL((k_lora_expand<T, MB, 2, STREAM>), grid, wg, 0, s, p);
+  else hipLaunchKernelGGL((k_lora_expand<T, MB, 4, STREAM>), grid, wg, 0, s, p);
   return hipGetLastError();
+}
+
+template <typename T, int MB>
+hipError_t expand(const LArgs& p, hipStream_t s) {
+  const bool stream = p.t * p.n * (int64_t)sizeof(T) >= kStreamBytes && p.n % 8 == 0;
+  return stream ? expand_as<T, MB, true>(p, s) : expand_as<T, MB, false>(p, s);
 }
 
 }  // namespace
@@ -287,11 +390,11 @@ hipError_t launch_lora(const uint16_t* x, int64_t t, int64_t k, const int32_t* o
   p.rank = (int)rank;
   p.rank_pad = pad16(rank);
   p.parts = lora_parts(t, adapters, rank, k);
-  const bool wide = lora_shift(t) == 6;
-  const hipError_t e = wide ? shrink<4>(p, s) : shrink<1>(p, s);
+  const int sh = shrink_shift(t), ex = expand_shift(t);
+  const hipError_t e = sh == 6 ? shrink<4>(p, s) : sh == 5 ? shrink<2>(p, s) : shrink<1>(p, s);
   if (e != hipSuccess) return e;
-  if (out_bf16) return wide ? expand<__bf16, 4>(p, s) : expand<__bf16, 1>(p, s);
-  return wide ? expand<float, 4>(p, s) : expand<float, 1>(p, s);
+  if (out_bf16) return ex == 5 ? expand<__bf16, 2>(p, s) : expand<__bf16, 1>(p, s);
+  return ex == 5 ? expand<float, 2>(p, s) : expand<float, 1>(p, s);
 }
 
 }  // namespace wq

@@ -175,11 +175,11 @@ __device__ __forceinline__ uint4 load16(const uint8_t* row, int64_t e, int64_t h
   return v;
 }
 
-template <int DT>
+template <int DT, bool STREAM>
 __device__ __forceinline__ void store16(uint8_t* row, int64_t e, int64_t h, uint4 v) {
   constexpr int VE = per_lane<DT>(), EB = elem_bytes<DT>();
   if (e + VE <= h) {
-    __builtin_memcpy(reinterpret_cast<Raw16*>(row + e * EB), &v, 16);
+    store_16<STREAM>(row + e * EB, uint32x4{v.x, v.y, v.z, v.w});
   } else {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -235,7 +235,7 @@ __device__ __forceinline__ bool move_lane(const MoveArgs& p, int& token, int64_t
   return token < p.t && e < p.h;
 }
 
-template <int DT>
+template <int DT, bool STREAM>
 __global__ __launch_bounds__(256) void k_dispatch_rows(MoveArgs p) {
   int token;
   int64_t e;
@@ -245,12 +245,12 @@ __global__ __launch_bounds__(256) void k_dispatch_rows(MoveArgs p) {
   const int* pl = p.place + (int64_t)token * p.topk;
   for (int j = 0; j < p.topk; ++j) {
     const int pos = pl[j];
-    if ((unsigned)pos < (unsigned)p.slots) store16<DT>(p.dst + pos * pitch, e, p.h, v);
+    if ((unsigned)pos < (unsigned)p.slots) store16<DT, STREAM>(p.dst + pos * pitch, e, p.h, v);
   }
 }
 
 // Four rows in flight per lane; summed in float32 in the order of j.
-template <int DT, bool WEIGHTED>
+template <int DT, bool WEIGHTED, bool STREAM>
 __global__ __launch_bounds__(256) void k_combine_rows(MoveArgs p) {
   constexpr int VE = per_lane<DT>(), JB = 4;
   int token;
@@ -283,7 +283,7 @@ __global__ __launch_bounds__(256) void k_combine_rows(MoveArgs p) {
         for (int i = 0; i < VE; ++i) acc[i] = WEIGHTED ? fmaf(w[u], f[i], acc[i]) : acc[i] + f[i];
       }
   }
-  store16<DT>(p.dst + token * pitch, e, p.h, pack<DT>(acc));
+  store16<DT, STREAM>(p.dst + token * pitch, e, p.h, pack<DT>(acc));
 }
 
 struct GradArgs {
@@ -300,7 +300,7 @@ struct GradArgs {
 // LANES (64 or 256) lanes walk one token's row; each 16 bytes of d_out meet up
 // to JB rows at a time: the scaled copy goes out, the product with the row
 // goes into that row's sum.  The sums join in a fixed order.
-template <int DT, int LANES>
+template <int DT, int LANES, bool STREAM>
 __global__ __launch_bounds__(256) void k_combine_rows_grad(GradArgs p) {
   constexpr int VE = per_lane<DT>(), JB = 4, WAVES = LANES / 64;
   __shared__ float part[WAVES > 1 ? WAVES : 1][JB];
@@ -337,7 +337,7 @@ __global__ __launch_bounds__(256) void k_combine_rows_grad(GradArgs p) {
             g[i] = w[u] * d[i];
             dot[u] = fmaf(d[i], f[i], dot[u]);
           }
-          store16<DT>(p.d_rows + pos[u] * pitch, e, p.h, pack<DT>(g));
+          store16<DT, STREAM>(p.d_rows + pos[u] * pitch, e, p.h, pack<DT>(g));
         }
     }
 #pragma unroll
@@ -364,6 +364,12 @@ __global__ __launch_bounds__(256) void k_combine_rows_grad(GradArgs p) {
   }
 }
 
+// whole 16-byte pieces only: the ones that straddle two lines came out 3% slower
+template <int DT>
+bool streams(int64_t rows, int64_t h) {
+  return rows * h * elem_bytes<DT>() >= kStreamBytes && h % per_lane<DT>() == 0;
+}
+
 template <int DT>
 unsigned move_grid(MoveArgs& p) {
   const int64_t nv = (p.h + per_lane<DT>() - 1) / per_lane<DT>();
@@ -376,27 +382,37 @@ unsigned move_grid(MoveArgs& p) {
 
 template <int DT>
 hipError_t dispatch(MoveArgs p, hipStream_t s) {
-  const unsigned grid = move_grid<DT>(p);
-  hipLaunchKernelGGL(k_dispatch_rows<DT>, dim3(grid), dim3(256), 0, s, p);
+  const dim3 grid(move_grid<DT>(p)), wg(256);
+  if (streams<DT>(p.slots, p.h)) hipLaunchKernelGGL((k_dispatch_rows<DT, true>), grid, wg, 0, s, p);
+  else hipLaunchKernelGGL((k_dispatch_rows<DT, false>), grid, wg, 0, s, p);
+  return hipGetLastError();
+}
+
+template <int DT, bool WEIGHTED>
+hipError_t combine_as(MoveArgs p, hipStream_t s) {
+  const dim3 grid(move_grid<DT>(p)), wg(256);
+  if (streams<DT>(p.t, p.h)) hipLaunchKernelGGL((k_combine_rows<DT, WEIGHTED, true>), grid, wg, 0, s, p);
+  else hipLaunchKernelGGL((k_combine_rows<DT, WEIGHTED, false>), grid, wg, 0, s, p);
   return hipGetLastError();
 }
 
 template <int DT>
-hipError_t combine(MoveArgs p, hipStream_t s) {
-  const unsigned grid = move_grid<DT>(p);
-  if (p.weights) hipLaunchKernelGGL((k_combine_rows<DT, true>), dim3(grid), dim3(256), 0, s, p);
-  else hipLaunchKernelGGL((k_combine_rows<DT, false>), dim3(grid), dim3(256), 0, s, p);
+hipError_t combine(const MoveArgs& p, hipStream_t s) {
+  return p.weights ? combine_as<DT, true>(p, s) : combine_as<DT, false>(p, s);
+}
+
+template <int DT, int LANES>
+hipError_t combine_grad_as(const GradArgs& p, hipStream_t s) {
+  const dim3 grid((unsigned)((p.t + 256 / LANES - 1) / (256 / LANES))), wg(256);
+  if (streams<DT>(p.slots, p.h)) hipLaunchKernelGGL((k_combine_rows_grad<DT, LANES, true>), grid, wg, 0, s, p);
+  else hipLaunchKernelGGL((k_combine_rows_grad<DT, LANES, false>), grid, wg, 0, s, p);
   return hipGetLastError();
 }
 
+// a wave walks a row of up to two of its strides; longer rows take a workgroup
 template <int DT>
 hipError_t combine_grad(const GradArgs& p, hipStream_t s) {
-  // a wave walks a row of up to two of its strides; longer rows take a workgroup
-  if (p.h <= 128 * per_lane<DT>())
-    hipLaunchKernelGGL((k_combine_rows_grad<DT, 64>), dim3((unsigned)((p.t + 3) / 4)), dim3(256), 0, s, p);
-  else
-    hipLaunchKernelGGL((k_combine_rows_grad<DT, 256>), dim3((unsigned)p.t), dim3(256), 0, s, p);
-  return hipGetLastError();
+  return p.h <= 128 * per_lane<DT>() ? combine_grad_as<DT, 64>(p, s) : combine_grad_as<DT, 256>(p, s);
 }
 
 }  // namespace
@@ -452,7 +468,7 @@ hipError_t launch_combine_rows(const void* rows, int dtype, const int32_t* place
 hipError_t launch_combine_rows_grad(const void* d_out, const void* rows, int dtype, const int32_t* place,
                                     const float* weights, int64_t t, int64_t topk, int64_t h, void* d_rows,
                                     float* d_weights, hipStream_t s) {
-  GradArgs p;
+  GradArgs p{};
   p.d_out = (const uint8_t*)d_out;
   p.rows = (const uint8_t*)rows;
   p.place = place;

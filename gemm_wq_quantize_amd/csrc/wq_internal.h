@@ -78,6 +78,25 @@ __device__ __forceinline__ void wait_vmcnt() {
   __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4) | (15 << 8));
 }
 
+// ---- 16-byte stores at the element's own alignment (global accesses need no
+// more on gfx950), optionally non-temporal.  An output beyond the L2s (32 MiB
+// over the XCDs) is not read back from them, and streaming it past them leaves
+// them to the inputs: rows moved there and back (755 MB) 166 -> 142 us, their
+// gradient (873 MB) 180 -> 170, adapters of a prompt (42 MB out) 78 -> 57.  A
+// smaller one is left in L2 for the kernel that reads it next.
+typedef uint32_t uint32x4_unaligned __attribute__((ext_vector_type(4), aligned(2)));
+typedef uint32_t uint32x4 __attribute__((ext_vector_type(4)));
+constexpr int64_t kStreamBytes = int64_t(32) << 20;
+
+// STREAM is a template argument because a branch between the two stores is folded
+// into the plain one.
+template <bool STREAM>
+__device__ __forceinline__ void store_16(void* dst, uint32x4 v) {
+  uint32x4_unaligned* p = reinterpret_cast<uint32x4_unaligned*>(dst);
+  if constexpr (STREAM) __builtin_nontemporal_store((uint32x4_unaligned)v, p);
+  else *p = v;
+}
+
 // Host-side per-device caches.  Each entry is an atomic, so concurrent first
 // calls from several host threads are well defined (at worst both query the
 // runtime and store the same value).

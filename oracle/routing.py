@@ -90,7 +90,9 @@ def lora(x, ids, a, b, scales, base):
     """out[i] = base[i] + scales[l] * b[l] (a[l] x[i]) with l = ids[i]; base[i]
     alone where ids[i] names no adapter."""
     out = np.array(base, dtype=np.float64)
-    for i, l in enumerate(np.asarray(ids).reshape(-1).tolist()):
-        if 0 <= l < a.shape[0]:
-            out[i] += float(scales[l]) * (b[l].astype(np.float64) @ (a[l].astype(np.float64) @ x[i].astype(np.float64)))
+    flat = np.asarray(ids).reshape(-1)
+    for l in range(a.shape[0]):
+        rows = np.flatnonzero(flat == l)
+        low = x[rows].astype(np.float64) @ a[l].astype(np.float64).T
+        out[rows] += float(scales[l]) * (low @ b[l].astype(np.float64).T)
     return out

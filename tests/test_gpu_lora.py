@@ -47,10 +47,10 @@ def check(c, ids, dt):
     # steps; a[l] x carried to the second product within 2^-17 (bf16 out) or 2^-24
     mag = routing.lora(np.abs(f(c["x"])), ids, np.abs(f(c["a"])), np.abs(f(c["b"])), np.abs(f(c["scales"])), 0 * base)
     low = np.zeros((t, n))
+    a, b, x = f(c["a"]), np.abs(f(c["b"])), f(c["x"])
     for i, l in enumerate(ids):
-        if 0 <= l < c["a"].shape[0]:
-            v = np.abs(f(c["a"])[l] @ f(c["x"])[i])
-            low[i] = abs(float(c["scales"][l])) * (np.abs(f(c["b"])[l]) @ v)
+        if 0 <= l < a.shape[0]:
+            low[i] = abs(float(c["scales"][l])) * (b[l] @ np.abs(a[l] @ x[i]))
     bound = torch.finfo(DT[dt]).eps / 2 * (np.abs(ref) + np.abs(ref - base) * 2.0 ** -8)
     bound += 8 * np.sqrt(k) * 2.0 ** -24 * mag + 2.0 ** (-17 if dt == "bf16" else -24) * low + 2.0 ** -24 * np.abs(base)
     bad = np.abs(got - ref) > bound
