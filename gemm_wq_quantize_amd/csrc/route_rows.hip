@@ -11,22 +11,31 @@ namespace {
 
 // ---------------------------------------------------------------- the sort
 //
-// One 512-lane workgroup sorts SORT_CHUNK slots: each of its 8 waves takes 512
-// consecutive slots, 64 at a time.  A wave finds the lanes that share a key
+// One 512-lane workgroup sorts a chunk of 512 IT slots: each of its 8 waves takes
+// 64 IT consecutive slots, 64 at a time.  A wave finds the lanes that share a key
 // with one ballot per key bit, so a slot's rank among them comes from the
 // lane order and the result is stable with no atomic whose order matters; one
 // LDS counter per (wave, bin) carries the count from one 64 to the next.  Two
 // scans (over the waves of a bin, then over the bins) turn the counters into
 // positions.  With more than one chunk a counting launch goes first, and each
 // workgroup sums the counts of the chunks before its own by itself: a third
-// launch for that sum would cost more than these reads from L2 (32 chunks of
+// launch for that sum would cost more than these reads from L2 (64 chunks of
 // 257 counters at 131072 slots in 256 bins).
-constexpr int SORT_THREADS = 512, SORT_WAVES = SORT_THREADS / 64, SORT_IT = 8;
-constexpr int SORT_CHUNK = SORT_THREADS * SORT_IT;
+constexpr int SORT_THREADS = 512, SORT_WAVES = SORT_THREADS / 64;
+
+// IT = 8 while one workgroup holds all slots (one launch), and again where the
+// chunks' counters are many: placing 131072 slots takes 8.7 us with IT = 4
+// against 11.1, 1048576 slots 26 against 21.
+int sort_it(int64_t slots) { return slots <= SORT_THREADS * 8 || slots > 524288 ? 8 : 4; }
+int64_t sort_blocks(int64_t slots) {
+  const int64_t chunk = SORT_THREADS * sort_it(slots);
+  return slots > 0 ? (slots + chunk - 1) / chunk : 1;
+}
 constexpr int SORT_BPT = (kMaxBins + 1 + SORT_THREADS - 1) / SORT_THREADS;  // counters per lane, at most
 
 __device__ __forceinline__ int sort_key(int id, int bins) { return (unsigned)id < (unsigned)bins ? id : bins; }
 
+template <int IT>
 __global__ __launch_bounds__(SORT_THREADS) void k_sort_count(const int* __restrict__ ids, int slots, int bins,
                                                              int* __restrict__ counts) {
   __shared__ int hist[kMaxBins + 1];
@@ -34,14 +43,15 @@ __global__ __launch_bounds__(SORT_THREADS) void k_sort_count(const int* __restri
   for (int i = threadIdx.x; i < nb; i += SORT_THREADS) hist[i] = 0;
   __syncthreads();
 #pragma unroll
-  for (int it = 0; it < SORT_IT; ++it) {
-    const int s = (int)blockIdx.x * SORT_CHUNK + it * SORT_THREADS + (int)threadIdx.x;
+  for (int it = 0; it < IT; ++it) {
+    const int s = (int)blockIdx.x * (SORT_THREADS * IT) + it * SORT_THREADS + (int)threadIdx.x;
     if (s < slots) atomicAdd(&hist[sort_key(ids[s], bins)], 1);
   }
   __syncthreads();
   for (int i = threadIdx.x; i < nb; i += SORT_THREADS) counts[(int64_t)blockIdx.x * nb + i] = hist[i];
 }
 
+template <int IT>
 __global__ __launch_bounds__(SORT_THREADS) void k_sort_place(const int* __restrict__ ids, int slots, int bins,
                                                              int key_bits, const int* __restrict__ counts,
                                                              int* __restrict__ offsets, int* __restrict__ order,
@@ -51,13 +61,30 @@ __global__ __launch_bounds__(SORT_THREADS) void k_sort_place(const int* __restri
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, nb = bins + 1;
   const int blk = blockIdx.x, nblk = gridDim.x;
   for (int i = tid; i < SORT_WAVES * nb; i += SORT_THREADS) hist[i] = 0;
+  // this lane's bins b0 .. b0 + bpt - 1: their counts in all chunks and in those
+  // before this one (first, so that the loads overlap)
+  const int bpt = (nb + SORT_THREADS - 1) / SORT_THREADS;
+  const int b0 = tid * bpt;
+  int all[SORT_BPT], before[SORT_BPT];
+#pragma unroll
+  for (int u = 0; u < SORT_BPT; ++u) {
+    all[u] = before[u] = 0;
+    if (nblk > 1 && u < bpt && b0 + u < nb) {
+#pragma unroll 16
+      for (int q = 0; q < nblk; ++q) {
+        const int c = counts[(int64_t)q * nb + b0 + u];
+        all[u] += c;
+        before[u] += q < blk ? c : 0;
+      }
+    }
+  }
   __syncthreads();
 
-  const int s0 = blk * SORT_CHUNK + wave * (64 * SORT_IT) + lane;
+  const int s0 = blk * (SORT_THREADS * IT) + wave * (64 * IT) + lane;
   int* mine = hist + wave * nb;
-  int tag[SORT_IT];  // key | position among the wave's slots of that key << 11
+  int tag[IT];  // key | position among the wave's slots of that key << 11
 #pragma unroll
-  for (int it = 0; it < SORT_IT; ++it) {
+  for (int it = 0; it < IT; ++it) {
     const int s = s0 + it * 64;
     const bool live = s < slots;
     const int key = live ? sort_key(ids[s], bins) : bins;
@@ -76,13 +103,11 @@ __global__ __launch_bounds__(SORT_THREADS) void k_sort_place(const int* __restri
   }
   __syncthreads();
 
-  // this lane's bins b0 .. b0 + bpt - 1: waves scanned in place, then the bins
-  const int bpt = (nb + SORT_THREADS - 1) / SORT_THREADS;
-  const int b0 = tid * bpt;
-  int before[SORT_BPT], total[SORT_BPT], sum = 0;
+  // waves scanned in place, then the bins
+  int total[SORT_BPT], sum = 0;
 #pragma unroll
   for (int u = 0; u < SORT_BPT; ++u) {
-    before[u] = total[u] = 0;
+    total[u] = 0;
     const int b = b0 + u;
     if (u < bpt && b < nb) {
       int run = 0;
@@ -93,17 +118,7 @@ __global__ __launch_bounds__(SORT_THREADS) void k_sort_place(const int* __restri
         run += c;
       }
       total[u] = run;
-      if (nblk > 1) {
-        int all = 0, pre = 0;
-#pragma unroll 8
-        for (int q = 0; q < nblk; ++q) {
-          const int c = counts[(int64_t)q * nb + b];
-          all += c;
-          pre += q < blk ? c : 0;
-        }
-        total[u] = all;
-        before[u] = pre;
-      }
+      if (nblk > 1) total[u] = all[u];
       sum += total[u];
     }
   }
@@ -131,7 +146,7 @@ __global__ __launch_bounds__(SORT_THREADS) void k_sort_place(const int* __restri
   __syncthreads();
 
 #pragma unroll
-  for (int it = 0; it < SORT_IT; ++it) {
+  for (int it = 0; it < IT; ++it) {
     const int s = s0 + it * 64;
     if (s < slots) {
       const int key = tag[it] & 2047;
@@ -418,24 +433,29 @@ hipError_t combine_grad(const GradArgs& p, hipStream_t s) {
 }  // namespace
 
 size_t sort_rows_workspace(int64_t slots, int64_t bins) {
-  const int64_t blocks = (slots + SORT_CHUNK - 1) / SORT_CHUNK;
+  const int64_t blocks = sort_blocks(slots);
   return blocks > 1 ? (size_t)(blocks * (bins + 1)) * sizeof(int) : 0;
+}
+
+template <int IT>
+static hipError_t sort_rows(const int32_t* ids, int slots, int bins, int32_t* offsets, int32_t* order, int32_t* place,
+                            int* ws, hipStream_t s) {
+  const dim3 blocks((unsigned)sort_blocks(slots)), wg(SORT_THREADS);
+  int bits = 1;
+  while ((bins >> bits) != 0) ++bits;  // keys 0 .. bins
+  if (blocks.x > 1) {
+    hipLaunchKernelGGL(k_sort_count<IT>, blocks, wg, 0, s, ids, slots, bins, ws);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  hipLaunchKernelGGL(k_sort_place<IT>, blocks, wg, 0, s, ids, slots, bins, bits, ws, offsets, order, place);
+  return hipGetLastError();
 }
 
 hipError_t launch_sort_rows(const int32_t* ids, int64_t slots, int64_t bins, int32_t* offsets, int32_t* order,
                             int32_t* place, void* ws, hipStream_t s) {
-  const unsigned blocks = slots > 0 ? (unsigned)((slots + SORT_CHUNK - 1) / SORT_CHUNK) : 1u;
-  int bits = 1;
-  while ((bins >> bits) != 0) ++bits;  // keys 0 .. bins
-  if (blocks > 1) {
-    hipLaunchKernelGGL(k_sort_count, dim3(blocks), dim3(SORT_THREADS), 0, s, ids, (int)slots, (int)bins,
-                       (int*)ws);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-  }
-  hipLaunchKernelGGL(k_sort_place, dim3(blocks), dim3(SORT_THREADS), 0, s, ids, (int)slots, (int)bins, bits,
-                     (const int*)ws, offsets, order, place);
-  return hipGetLastError();
+  return sort_it(slots) == 8 ? sort_rows<8>(ids, (int)slots, (int)bins, offsets, order, place, (int*)ws, s)
+                             : sort_rows<4>(ids, (int)slots, (int)bins, offsets, order, place, (int*)ws, s);
 }
 
 hipError_t launch_dispatch_rows(const void* x, int dtype, const int32_t* place, int64_t t, int64_t topk, int64_t h,

@@ -32,7 +32,8 @@ def check_sort(ids, bins):
 
 
 @pytest.mark.parametrize("t,topk,bins", [(0, 4, 5), (1, 1, 1), (1, 8, 128), (7, 9, 3), (64, 1, 2), (513, 8, 1024),
-                                         (4096, 1, 64), (4097, 1, 64), (3001, 7, 257), (20000, 2, 1), (9000, 6, 513)])
+                                         (4096, 1, 64), (4097, 1, 64), (3001, 7, 257), (20000, 2, 1), (9000, 6, 513),
+                                         (262145, 2, 100)])
 def test_sort(t, topk, bins):
     say("sort", t, topk, bins)
     rng = np.random.default_rng(1000 * t + bins)
