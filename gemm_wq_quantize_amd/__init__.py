@@ -358,11 +358,11 @@ def _at(t, dev):
     """The address of a contiguous tensor on device ``dev`` (None stays None)."""
     if t is None:
         return None
-    if not t.is_cuda:
-        raise ValueError("wq: tensors must be on the GPU")
-    if not t.is_contiguous():
-        raise ValueError("wq: tensors must be contiguous")
-    if t.get_device() != dev:
+    if t.get_device() != dev or not t.is_contiguous():
+        if not t.is_cuda:
+            raise ValueError("wq: tensors must be on the GPU")
+        if not t.is_contiguous():
+            raise ValueError("wq: tensors must be contiguous")
         raise ValueError(f"wq: tensor on {t.device}, stream on cuda:{dev}")
     return t.data_ptr()
 
@@ -420,7 +420,7 @@ def wq_sort_rows(ids, bins, offsets, order, place, workspace=None, stream=None):
     _require(order.numel() == t * topk and place.numel() == t * topk, "order and place hold t * topk values")
     d, raw = _where(stream)
     args = (_at(ids, d), t, topk, bins, _at(offsets, d), _at(order, d), _at(place, d))
-    ws, nbytes = _workspace("wq_sort_rows", stream, workspace, lib.wq_sort_rows_workspace(t, topk, bins))
+    ws, nbytes = _workspace("wq_sort_rows", stream, workspace, load_library().wq_sort_rows_workspace(t, topk, bins))
     _call("wq_sort_rows", d, raw, *args, _at(ws, d), nbytes)
 
 
@@ -528,7 +528,7 @@ def wq_lora(x, order, offsets, a, b, scales, base, out, workspace=None, stream=N
     d, raw = _where(stream)
     args = (_at(x, d), t, k, _at(order, d), _at(offsets, d), n_ad, _at(a, d), _at(b, d), rank, _at(scales, d),
             _at(base, d), _at(out, d), _dtype(out), n)
-    ws, nbytes = _workspace("wq_lora", stream, workspace, lib.wq_lora_workspace(t, k, n_ad, rank))
+    ws, nbytes = _workspace("wq_lora", stream, workspace, load_library().wq_lora_workspace(t, k, n_ad, rank))
     _call("wq_lora", d, raw, *args, _at(ws, d), nbytes)
 
 

@@ -22,11 +22,12 @@ typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
 // -------------------------------------------------------------- few rows a tile
 //
-// Bound by the weights' bytes.  A workgroup takes a tile of up to 16 rows and
-// 64 CB columns.  The rows sit in LDS, a slab of k at a time, so what flows
+// Bound by the weights' bytes (369 MB of 64 experts, k = 4096, n = 2816, 256 rows:
+// 83 us, 4.5 TB/s; a bare stream of them 57 to 72).  A workgroup takes a tile of
+// up to 16 rows and 64 CB columns.  The rows sit in LDS, a slab of k at a time, so what flows
 // through the vector memory path is the packed weights alone: each of the four
-// waves streams 16 CB columns over all of k from memory straight into
-// registers, DEPTH chunks ahead (a chunk is 32 LW k: 16 LW bytes of each
+// waves streams 16 CB columns over all of k (or all four the same 16, a quarter of
+// k each) from memory straight into registers, DEPTH chunks ahead (a chunk is 32 LW k: 16 LW bytes of each
 // column).  Products on v_mfma_f32_16x16x32_bf16: lane l holds 8 LW consecutive k
 // of column l % 16 (LW packed words) and reads the same k of row l % 16, so slot
 // k of MFMA w is k = chunk + 8 LW (l / 16) + 8 w + (0..7) on both sides.
@@ -83,15 +84,22 @@ __device__ __forceinline__ bf16x8 codes8(uint32_t w, uint32_t magic_v) {
   return __builtin_bit_cast(bf16x8, r);
 }
 
-constexpr int DEPTH = 4;             // chunks in flight per wave; also the chunks one scale load covers
 constexpr int FEW_LDS = 40 * 1024;   // a slab of rows and its row sums: four workgroups on a CU
 constexpr int FEW_SHIFT = 4, FEW_ROWS = 1 << FEW_SHIFT;
-static_assert((FEW_LDS - FEW_ROWS * 16) / (FEW_ROWS * 256 + FEW_ROWS * 4) >= DEPTH, "a slab holds DEPTH chunks");
 
-template <int CB, int LW, bool Z>
+// KS = 4: the waves of a workgroup share its 16 CB columns and take groups of
+// DEPTH chunks in turn, joining their sums at the end; KS = 1: each has columns
+// of its own.  A wave with its own columns takes 32 chunks of k = 4096 one after
+// the other, 5 us however little there is to do.  DEPTH: chunks in flight per wave
+// (8 with one block of columns: 45 us against 48 for 64 rows of 64 experts).
+template <int CB, int KS> constexpr int few_cols() { return 64 * CB / KS; }
+
+template <int CB, int KS, int DEPTH, int LW, bool Z>
 __global__ __launch_bounds__(256) void k_experts_few(EArgs p) {
   typedef typename Words<LW>::type words_t;
   constexpr int CH_K = 32 * LW, CH_BYTES = CH_K * 2;  // k of a chunk, bytes of it in a row of A
+  constexpr int SETS = DEPTH / 4, STRIDE = KS * DEPTH;  // chunks between a wave's groups
+  static_assert((FEW_LDS - FEW_ROWS * 16) / (FEW_ROWS * CH_BYTES + FEW_ROWS * 4) >= DEPTH, "a slab holds DEPTH chunks");
   __shared__ __attribute__((aligned(16))) uint8_t smem[FEW_LDS];
   __shared__ int src[FEW_ROWS];
   const int tid = threadIdx.x, lane = tid & 63;
@@ -103,7 +111,8 @@ __global__ __launch_bounds__(256) void k_experts_few(EArgs p) {
 
   // ---- the weights' first chunks are on their way before anything else
   const int lr = lane & 15, lq = lane >> 4;
-  const int64_t n0 = ((int64_t)tn * 4 + wave) * (16 * CB);
+  const int64_t n0 = (int64_t)tn * few_cols<CB, KS>() + (KS == 1 ? wave * (16 * CB) : 0);
+  int ch = KS == 1 ? 0 : wave * DEPTH;  // this wave's next group
   const int nch = (int)(p.k / CH_K);
   const uint8_t* brow[CB];
   int64_t srow[CB];
@@ -114,23 +123,27 @@ __global__ __launch_bounds__(256) void k_experts_few(EArgs p) {
     srow[j] = col * p.ngroups;
   }
   words_t w[DEPTH][CB];
-  uint16_t sc[2][CB], zc[2][CB];  // lane quarter q: the scale (zero) of chunk 4 (ch / 4) + q
+  // lane quarter q: the scales (zeros) of chunks q, 4 + q of this DEPTH and the next
+  uint16_t sc[2][SETS][CB], zc[2][SETS][CB];
   auto load = [&](int ch, words_t (&f)[CB]) {
 #pragma unroll
     for (int j = 0; j < CB; ++j) f[j] = *reinterpret_cast<const words_t*>(brow[j] + (int64_t)ch * (CH_K / 2));
   };
-  auto load_s = [&](int ch, uint16_t (&s)[CB], uint16_t (&z)[CB]) {
-    const int64_t g = min(ch + lq, nch - 1) / p.group_chunks;
+  auto load_s = [&](int ch, int to) {
 #pragma unroll
-    for (int j = 0; j < CB; ++j) {
-      s[j] = p.scales[srow[j] + g];
-      if (Z) z[j] = p.zeros[srow[j] + g];
+    for (int c = 0; c < SETS; ++c) {
+      const int64_t g = min(ch + 4 * c + lq, nch - 1) / p.group_chunks;
+#pragma unroll
+      for (int j = 0; j < CB; ++j) {
+        sc[to][c][j] = p.scales[srow[j] + g];
+        if (Z) zc[to][c][j] = p.zeros[srow[j] + g];
+      }
     }
   };
 #pragma unroll
   for (int d = 0; d < DEPTH; ++d)
-    if (d < nch) load(d, w[d]);
-  load_s(0, sc[0], zc[0]);
+    if (ch + d < nch) load(ch + d, w[d]);
+  load_s(ch, 0);
   if (tid < t.rows) src[tid] = (int)a_row(p, t.row0 + tid);
   __syncthreads();
 
@@ -159,20 +172,20 @@ __global__ __launch_bounds__(256) void k_experts_few(EArgs p) {
       *reinterpret_cast<u32x4*>(smem + row * pitch + c * 16) = v;
     }
     __syncthreads();
-    for (int ch = wave; ch < c1 - c0; ch += 4) {
+    for (int at = wave; at < c1 - c0; at += 4) {
       floatx4 r = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int u = 0; u < LW; ++u)
         r = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-            *reinterpret_cast<const bf16x8*>(a_rd + ch * CH_BYTES + u * 16), ones, r, 0, 0, 0);
-      if (lr == 0) *reinterpret_cast<floatx4*>(rs + ch * FEW_ROWS + lq * 4) = r;
+            *reinterpret_cast<const bf16x8*>(a_rd + at * CH_BYTES + u * 16), ones, r, 0, 0, 0);
+      if (lr == 0) *reinterpret_cast<floatx4*>(rs + at * FEW_ROWS + lq * 4) = r;
     }
     __syncthreads();
 
     // FULL: all DEPTH chunks and all that their loads fetch exist
-    auto group = [&](auto full, int ch) {
+    auto group = [&](auto full) {
       constexpr bool FULL = decltype(full)::value;
-      if (FULL || ch + DEPTH < nch) load_s(ch + DEPTH, sc[1], zc[1]);
+      if (FULL || ch + STRIDE < nch) load_s(ch + STRIDE, 1);
 #pragma unroll
       for (int d = 0; d < DEPTH; ++d) {
         if (!FULL && ch + d >= c1) break;
@@ -187,25 +200,35 @@ __global__ __launch_bounds__(256) void k_experts_few(EArgs p) {
           for (int j = 0; j < CB; ++j)
             sum[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, codes8(w[d][j][u], magic_v), sum[j], 0, 0, 0);
         }
-        if (FULL || ch + d + DEPTH < nch) load(ch + d + DEPTH, w[d]);
+        if (FULL || ch + d + STRIDE < nch) load(ch + d + STRIDE, w[d]);
         const floatx4 r = *reinterpret_cast<const floatx4*>(rs + at * FEW_ROWS + lq * 4);
 #pragma unroll
         for (int j = 0; j < CB; ++j) {
-          const float s = bf16_to_f32((uint32_t)__shfl((int)sc[0][j], d * 16 + lr));
-          const float zb = 128.f + (Z ? bf16_to_f32((uint32_t)__shfl((int)zc[0][j], d * 16 + lr)) : p.zero_const);
+          const float s = bf16_to_f32((uint32_t)__shfl((int)sc[0][d / 4][j], d % 4 * 16 + lr));
+          const float zb = 128.f + (Z ? bf16_to_f32((uint32_t)__shfl((int)zc[0][d / 4][j], d % 4 * 16 + lr)) : p.zero_const);
 #pragma unroll
           for (int e = 0; e < 4; ++e) acc[j][e] = fmaf(s, fmaf(-zb, r[e], sum[j][e]), acc[j][e]);
         }
       }
 #pragma unroll
-      for (int j = 0; j < CB; ++j) {
-        sc[0][j] = sc[1][j];
-        if (Z) zc[0][j] = zc[1][j];
-      }
+      for (int c = 0; c < SETS; ++c)
+#pragma unroll
+        for (int j = 0; j < CB; ++j) {
+          sc[0][c][j] = sc[1][c][j];
+          if (Z) zc[0][c][j] = zc[1][c][j];
+        }
     };
-    int ch = c0;
-    for (; ch + DEPTH <= c1 && ch + 2 * DEPTH <= nch; ch += DEPTH) group(std::true_type{}, ch);
-    for (; ch < c1; ch += DEPTH) group(std::false_type{}, ch);
+    for (; ch + DEPTH <= c1 && ch + STRIDE + DEPTH <= nch; ch += STRIDE) group(std::true_type{});
+    for (; ch < c1; ch += STRIDE) group(std::false_type{});
+  }
+  if constexpr (KS > 1) {  // join the waves' sums, in the order of the waves
+    static_assert(CB == 1, "one column block");
+    floatx4* part = reinterpret_cast<floatx4*>(smem);
+    __syncthreads();
+    part[wave * 64 + lane] = acc[0];
+    __syncthreads();
+    if (wave > 0) return;
+    acc[0] = (part[lane] + part[64 + lane]) + (part[128 + lane] + part[192 + lane]);
   }
   // element e of lane l is row 4 (l / 16) + e, column l % 16
 #pragma unroll
@@ -219,12 +242,12 @@ __global__ __launch_bounds__(256) void k_experts_few(EArgs p) {
     }
 }
 
-template <int CB, int LW>
-hipError_t launch_few(EArgs p, hipStream_t s) {
-  p.tiles_n = (int)((p.n + 64 * CB - 1) / (64 * CB));
+template <int CB, int KS, int DEPTH, int LW>
+hipError_t launch_few_as(EArgs p, hipStream_t s) {
+  p.tiles_n = (int)((p.n + few_cols<CB, KS>() - 1) / few_cols<CB, KS>());
   const dim3 grid((unsigned)(row_tiles_bound(p.slots, p.experts, FEW_SHIFT) * p.tiles_n));
-  if (p.zeros) hipLaunchKernelGGL((k_experts_few<CB, LW, true>), grid, dim3(256), 0, s, p);
-  else hipLaunchKernelGGL((k_experts_few<CB, LW, false>), grid, dim3(256), 0, s, p);
+  if (p.zeros) hipLaunchKernelGGL((k_experts_few<CB, KS, DEPTH, LW, true>), grid, dim3(256), 0, s, p);
+  else hipLaunchKernelGGL((k_experts_few<CB, KS, DEPTH, LW, false>), grid, dim3(256), 0, s, p);
   return hipGetLastError();
 }
 
@@ -529,6 +552,18 @@ hipError_t launch_tiles(EArgs p, hipStream_t s) {
   return hipGetLastError();
 }
 
+// Below 256 workgroups of 64 columns the waves share columns (k = 4096, n = 2816: 9.0
+// us against 10.8 for 4 rows of as many experts, 15.8 against 14.5 for 8).  From
+// 6 rows an expert on two column blocks a wave share the LDS reads of A (97 us
+// against 101 for 512 rows of 64 experts, 86 against 83 for 256).
+template <int LW>
+hipError_t launch_few(const EArgs& p, hipStream_t s) {
+  const int64_t wgs = row_tiles_bound(p.slots, p.experts, FEW_SHIFT) * ((p.n + 63) / 64);
+  if (wgs < 256) return launch_few_as<1, 4, 4, LW>(p, s);
+  if (p.slots / p.experts >= 6 && wgs >= 2048) return launch_few_as<2, 1, 4, LW>(p, s);
+  return launch_few_as<1, 1, 8, LW>(p, s);
+}
+
 }  // namespace
 
 hipError_t launch_gemm_w4a16_experts(const uint16_t* a, int64_t a_rows, const int32_t* order, int64_t topk,
@@ -562,17 +597,9 @@ hipError_t launch_gemm_w4a16_experts(const uint16_t* a, int64_t a_rows, const in
                     zero_const * 8.f == std::nearbyint(zero_const * 8.f);
     return launch_tiles(p, s);
   }
-  // 128-k chunks, or 64-k ones where a group or k is no multiple of 128.  Two
-  // column blocks a wave (which share the LDS reads of A) where that leaves four
-  // workgroups a CU: 97 us against 107 with one block at 512 rows of 64 experts
-  // (k = 4096, n = 2816), but 15.2 against 14.1 at 8 rows.
-  const bool wide = row_tiles_bound(slots, experts, FEW_SHIFT) * (n / 128) >= 1024;
-  if (group % 128 == 0) {
-    p.group_chunks = (int)(group / 128);
-    return wide ? launch_few<2, 4>(p, s) : launch_few<1, 4>(p, s);
-  }
-  p.group_chunks = (int)(group / 64);
-  return wide ? launch_few<2, 2>(p, s) : launch_few<1, 2>(p, s);
+  // 128-k chunks, or 64-k ones where a group or k is no multiple of 128
+  p.group_chunks = (int)(group % 128 == 0 ? group / 128 : group / 64);
+  return group % 128 == 0 ? launch_few<4>(p, s) : launch_few<2>(p, s);
 }
 
 }  // namespace wq
