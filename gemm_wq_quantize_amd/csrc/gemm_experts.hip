@@ -72,18 +72,6 @@ template <int LW> struct Words;
 template <> struct Words<4> { typedef u32x4 type; };
 template <> struct Words<2> { typedef u32x2 type; };
 
-// eight codes of one word -> bf16x8 of (128 + q), k order.  In plain code, not asm:
-// the compiler then keeps the wait states that a matrix instruction needs
-// between the vector instruction that wrote its operand and itself.
-__device__ __forceinline__ bf16x8 codes8(uint32_t w, uint32_t magic_v) {
-  u32x4 r;
-  r[0] = (w & 0x000F000Fu) | magic_v;
-  r[1] = ((w >> 4) & 0x000F000Fu) | magic_v;
-  r[2] = ((w >> 8) & 0x000F000Fu) | magic_v;
-  r[3] = ((w >> 12) & 0x000F000Fu) | magic_v;
-  return __builtin_bit_cast(bf16x8, r);
-}
-
 constexpr int FEW_LDS = 40 * 1024;   // a slab of rows and its row sums: four workgroups on a CU
 constexpr int FEW_SHIFT = 4, FEW_ROWS = 1 << FEW_SHIFT;
 
@@ -198,7 +186,7 @@ __global__ __launch_bounds__(256) void k_experts_few(EArgs p) {
           const bf16x8 a = *reinterpret_cast<const bf16x8*>(a_rd + at * CH_BYTES + u * 16);
 #pragma unroll
           for (int j = 0; j < CB; ++j)
-            sum[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, codes8(w[d][j][u], magic_v), sum[j], 0, 0, 0);
+            sum[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, unpack8(w[d][j][u], magic_v), sum[j], 0, 0, 0);
         }
         if (FULL || ch + d + STRIDE < nch) load(ch + d + STRIDE, w[d]);
         const floatx4 r = *reinterpret_cast<const floatx4*>(rs + at * FEW_ROWS + lq * 4);

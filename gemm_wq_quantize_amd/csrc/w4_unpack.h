@@ -18,14 +18,18 @@ __device__ __forceinline__ uint32_t vconst(uint32_t c) {
   return r;
 }
 
-// eight codes of one gfx950-layout word -> bf16x8 of (128 + q), k order
+// eight codes of one gfx950-layout word -> bf16x8 of (128 + q), k order (magic_v
+// 0x43004300).  In plain code, not asm: what it returns goes straight into a matrix
+// instruction, and the compiler keeps the two wait states that needs after a
+// vector instruction that wrote its operand only where it knows the writer for
+// one (asm here left one, and in another kernel gave NaN).
 __device__ __forceinline__ bf16x8 unpack8(uint32_t w, uint32_t magic_v) {
   typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
   u32x4 r;
-  r[0] = and_or(w, 0x000F000Fu, magic_v);
-  r[1] = and_or(w >> 4, 0x000F000Fu, magic_v);
-  r[2] = and_or(w >> 8, 0x000F000Fu, magic_v);
-  r[3] = and_or(w >> 12, 0x000F000Fu, magic_v);
+  r[0] = (w & 0x000F000Fu) | magic_v;
+  r[1] = ((w >> 4) & 0x000F000Fu) | magic_v;
+  r[2] = ((w >> 8) & 0x000F000Fu) | magic_v;
+  r[3] = ((w >> 12) & 0x000F000Fu) | magic_v;
   return __builtin_bit_cast(bf16x8, r);
 }
 
