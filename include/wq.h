@@ -369,7 +369,8 @@ int64_t wq_sort_rows_workspace(int64_t t, int64_t topk, int64_t bins);
  *   workspace device memory of wq_sort_rows_workspace() bytes that nothing
  *             else uses until the call has run (NULL if that is 0).  Two
  *             captured graphs that may run at once need one each.
- * The result is a function of ids alone.  t == 0 writes offsets (all 0).
+ * The result is a function of ids alone.  t == 0 writes offsets (all 0).  The
+ * arrays must not overlap.
  * Requires 1 <= bins <= 1024, t * topk <= 2^24, pointers 4-byte aligned; a
  * workspace that is too small is WQ_EINVAL.
  */
@@ -384,7 +385,8 @@ int wq_sort_rows(const int32_t* ids, int64_t t, int64_t topk, int64_t bins, int3
  *         are left as they were.
  * Its gradient with respect to x is wq_combine_rows of out's gradient with
  * weights NULL.  Requires t * topk <= 2^24, h < 2^31, x and out aligned to
- * the element.
+ * the element (rows of any length; 16-byte aligned ones are fastest), at most
+ * 2^31 - 1 workgroups of 1024 elements.
  */
 int wq_dispatch_rows(const void* x, int dtype, const int32_t* place, int64_t t, int64_t topk, int64_t h, void* out,
                      void* stream);
@@ -462,8 +464,8 @@ int64_t wq_lora_workspace(int64_t t, int64_t k, int64_t adapters, int64_t rank);
  *   scales  [adapters] float32.
  *   base    [t][n], or NULL for zeros: the output of wq_gemv_w4 or
  *           wq_gemm_w4a16 for the same x.
- *   out     [t][n], may be base itself; out_dtype WQ_BF16 or WQ_F32, base has
- *           the same.
+ *   out     [t][n], may be base itself (or must not overlap it); out_dtype
+ *           WQ_BF16 or WQ_F32, base has the same.
  *   workspace as for wq_sort_rows, wq_lora_workspace() bytes.
  * Sums in float32, rounded once; a[l] x is carried to the second product with
  * 17 significant bits for bf16 out, all 24 for float32.  Finite x, a, b and

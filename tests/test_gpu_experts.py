@@ -149,3 +149,68 @@ def test_large_weight_offsets():
         # element 7 of a word is nibble 7, element 1 (8001 = 8 * 1000 + 1) nibble 4
         want = (last[:, 3] >> 4).float() - (last[:, 4002] & 15).float()
         assert torch.equal(out.float().cpu(), want.expand(t, n))
+
+
+@pytest.mark.parametrize("t", [4, 40, 300])
+def test_rows_do_not_mix(t):
+    """A row with NaN or infinity leaves the other rows' bits alone."""
+    say("rows do not mix", t)
+    n, k = 136, 512
+    c = case(t, 1, 2, n, k, 128, gather=False)
+    out = run(c, torch.empty((t, n), dtype=torch.bfloat16, device="cuda"))
+    c["a"][t // 2, 7] = float("nan")
+    c["a"][t - 1, 100] = float("inf")
+    bad = run(c, torch.empty((t, n), dtype=torch.bfloat16, device="cuda"))
+    keep = [i for i in range(t) if i not in (t // 2, t - 1)]
+    assert torch.equal(out[keep], bad[keep])
+    assert not torch.isfinite(bad[t // 2].float()).any() and not torch.isfinite(bad[t - 1].float()).any()
+
+
+def test_a_bad_plan_stays_in_its_buffers():
+    """Offsets and an order that were never written: whatever comes out, nothing
+    is read or written outside, and the rows behind the output are untouched."""
+    say("bad plan")
+    for t in (8, 200):
+        c = case(t, 2, 4, 64, 128, 128)
+        c["offsets"] = torch.tensor([-5, 3, 10 ** 9, 2, 2 ** 31 - 1], dtype=torch.int32)
+        c["order"] = torch.full((2 * t,), 2 ** 31 - 1, dtype=torch.int32)
+        c["order"][::3] = -2 ** 31
+        space = torch.zeros((2 * t + 64, 64), dtype=torch.bfloat16, device="cuda")
+        run(c, space[:2 * t])
+        torch.cuda.synchronize()
+        assert (space[2 * t:] == 0).all()
+
+
+def test_large_output_offsets():
+    """Rows of the output past 2^32 bytes."""
+    say("large output")
+    slots, n, k, e = 300000, 8192, 64, 3
+    gen = torch.Generator().manual_seed(4)
+    b = torch.randint(0, 256, (e, n, k // 2), dtype=torch.uint8, generator=gen)
+    a = torch.zeros((slots, k), dtype=torch.bfloat16, device="cuda")
+    a[:, 3] = 2.0
+    offsets = torch.tensor([0, 5, slots - 7, slots], dtype=torch.int32, device="cuda")
+    out = torch.empty((slots, n), dtype=torch.bfloat16, device="cuda")
+    g.wq_gemm_w4a16_experts(a, None, 1, offsets, b.cuda(), g.LAYOUT_GFX950,
+                            torch.ones((e, n, 1), dtype=torch.bfloat16, device="cuda"), None, k, 8.0, out)
+    for i, x in ((0, 0), (5, 1), (slots - 8, 1), (slots - 7, 2), (slots - 1, 2)):
+        want = 2.0 * ((b[x, :, 2] >> 4).float() - 8.0)    # element 3 is nibble 5
+        assert torch.equal(out[i].float().cpu(), want)
+
+
+def test_two_streams_at_once():
+    """Two calls in flight on streams of their own give what each gives alone."""
+    say("two streams")
+    n, k = 264, 1024
+    cases = [case(t, 2, 6, n, k, 128, seed=t) for t in (500, 7)]
+    alone = [run(c, torch.empty((2 * t, n), dtype=torch.bfloat16, device="cuda")) for c, t in zip(cases, (500, 7))]
+    outs = [torch.empty_like(a) for a in alone]
+    dev = [{x: v.cuda() if isinstance(v, torch.Tensor) else v for x, v in c.items()} for c in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for d, o, st in zip(dev, outs, streams):
+            g.wq_gemm_w4a16_experts(d["a"], d["order"], 2, d["offsets"], d["b"], g.LAYOUT_GFX950, d["scales"], d["zeros"],
+                                    128, 8.0, o, stream=st)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, o) for a, o in zip(alone, outs))

@@ -140,6 +140,37 @@ def test_large_offsets():
     assert torch.equal(out, (2.0 * (torch.arange(n, device="cuda") % 64)).expand(t, n))
 
 
+def test_a_bad_plan_stays_in_its_buffers():
+    say("bad plan")
+    for t in (9, 1500):
+        c, _ = case(t, 64, 40, 3, 16)
+        c["offsets"] = torch.tensor([-7, 10 ** 9, 3, 2 ** 31 - 1], dtype=torch.int32)
+        c["order"] = torch.full((t,), 2 ** 31 - 1, dtype=torch.int32)
+        c["order"][::2] = -5
+        space = torch.zeros((t + 64, 40), dtype=torch.bfloat16, device="cuda")
+        run(c, space[:t])
+        torch.cuda.synchronize()
+        assert (space == 0).all()              # no row of the order exists
+
+
+def test_refusals_on_the_device():
+    say("refusals")
+    c, _ = case(5, 64, 40, 3, 16)
+    d = {k: v.cuda() for k, v in c.items()}
+    out = torch.zeros((5, 40), dtype=torch.bfloat16, device="cuda")
+    call = lambda **kw: g.wq_lora(**{**d, "out": out, **kw})
+    with pytest.raises(ValueError, match="on the GPU"):
+        call(x=c["x"])
+    with pytest.raises(ValueError, match="contiguous"):
+        call(base=torch.zeros((40, 5), dtype=torch.bfloat16, device="cuda").T)
+    with pytest.raises(g.WqError, match="ESHAPE"):
+        call(a=torch.zeros((3, 20, 64), dtype=torch.bfloat16, device="cuda"),
+             b=torch.zeros((3, 40, 20), dtype=torch.bfloat16, device="cuda"))
+    with pytest.raises(g.WqError, match="EALIGN"):
+        call(workspace=torch.zeros(4096, dtype=torch.uint8, device="cuda")[4:])
+    assert (out == 0).all()
+
+
 def weights(e, n, k, gen):
     w = (0.02 * torch.randn((e * n, k), generator=gen)).half().cuda()
     packed = torch.empty((e * n, k // 2), dtype=torch.uint8, device="cuda")
