@@ -23,11 +23,11 @@ typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 // -------------------------------------------------------------- few rows a tile
 //
 // Bound by the weights' bytes (369 MB of 64 experts, k = 4096, n = 2816, 256 rows:
-// 83 us, 4.5 TB/s; a bare stream of them 57 to 72).  A workgroup takes a tile of
+// 81 us, 4.6 TB/s; a bare stream of them 57 to 72).  A workgroup takes a tile of
 // up to 16 rows and 64 CB columns.  The rows sit in LDS, a slab of k at a time, so what flows
 // through the vector memory path is the packed weights alone: each of the four
-// waves streams 16 CB columns over all of k (or all four the same 16, a quarter of
-// k each) from memory straight into registers, DEPTH chunks ahead (a chunk is 32 LW k: 16 LW bytes of each
+// waves streams 16 CB columns over all of k (or KS of them the same ones, a part
+// of k each) from memory straight into registers, DEPTH chunks ahead (a chunk is 32 LW k: 16 LW bytes of each
 // column).  Products on v_mfma_f32_16x16x32_bf16: lane l holds 8 LW consecutive k
 // of column l % 16 (LW packed words) and reads the same k of row l % 16, so slot
 // k of MFMA w is k = chunk + 8 LW (l / 16) + 8 w + (0..7) on both sides.
@@ -72,13 +72,12 @@ template <int LW> struct Words;
 template <> struct Words<4> { typedef u32x4 type; };
 template <> struct Words<2> { typedef u32x2 type; };
 
-constexpr int FEW_LDS = 40 * 1024;   // a slab of rows and its row sums: four workgroups on a CU
+constexpr int FEW_LDS = 40 * 1024 - 256;  // a slab of rows and its row sums: with src, four workgroups on a CU
 constexpr int FEW_SHIFT = 4, FEW_ROWS = 1 << FEW_SHIFT;
 
-// KS = 4: the waves of a workgroup share its 16 CB columns and take groups of
-// DEPTH chunks in turn, joining their sums at the end; KS = 1: each has columns
-// of its own.  A wave with its own columns takes 32 chunks of k = 4096 one after
-// the other, 5 us however little there is to do.  DEPTH: chunks in flight per wave
+// KS waves share 16 CB columns and take groups of DEPTH chunks in turn, joining
+// their sums at the end.  With KS = 1 a wave takes the 32 chunks of k = 4096 one
+// after the other, 5 us however little there is to do.  DEPTH: chunks in flight per wave
 // (8 with one block of columns: 45 us against 48 for 64 rows of 64 experts).
 template <int CB, int KS> constexpr int few_cols() { return 64 * CB / KS; }
 
@@ -99,8 +98,8 @@ __global__ __launch_bounds__(256) void k_experts_few(EArgs p) {
 
   // ---- the weights' first chunks are on their way before anything else
   const int lr = lane & 15, lq = lane >> 4;
-  const int64_t n0 = (int64_t)tn * few_cols<CB, KS>() + (KS == 1 ? wave * (16 * CB) : 0);
-  int ch = KS == 1 ? 0 : wave * DEPTH;  // this wave's next group
+  const int64_t n0 = (int64_t)tn * few_cols<CB, KS>() + wave / KS * (16 * CB);
+  int ch = wave % KS * DEPTH;  // this wave's next group
   const int nch = (int)(p.k / CH_K);
   const uint8_t* brow[CB];
   int64_t srow[CB];
@@ -215,8 +214,10 @@ __global__ __launch_bounds__(256) void k_experts_few(EArgs p) {
     __syncthreads();
     part[wave * 64 + lane] = acc[0];
     __syncthreads();
-    if (wave > 0) return;
-    acc[0] = (part[lane] + part[64 + lane]) + (part[128 + lane] + part[192 + lane]);
+    if (wave % KS > 0) return;
+    const floatx4* mine = part + wave * 64 + lane;
+    acc[0] = mine[0] + mine[64];
+    if (KS == 4) acc[0] += mine[128] + mine[192];
   }
   // element e of lane l is row 4 (l / 16) + e, column l % 16
 #pragma unroll
@@ -540,14 +541,16 @@ hipError_t launch_tiles(EArgs p, hipStream_t s) {
   return hipGetLastError();
 }
 
-// Below 256 workgroups of 64 columns the waves share columns (k = 4096, n = 2816: 9.0
-// us against 10.8 for 4 rows of as many experts, 15.8 against 14.5 for 8).  From
-// 6 rows an expert on two column blocks a wave share the LDS reads of A (97 us
-// against 101 for 512 rows of 64 experts, 86 against 83 for 256).
+// Below 512 workgroups of 64 columns two waves share columns, below 256 all four
+// (k = 4096, n = 2816: 12.1 us against 14.5 for 8 rows of as many experts, and 8.9
+// against 10.8 for 4).  From 6 rows an expert on two column blocks a wave share
+// the LDS reads of A (97 us against 101 for 512 rows of 64 experts, but 84
+// against 81 for 256).
 template <int LW>
 hipError_t launch_few(const EArgs& p, hipStream_t s) {
   const int64_t wgs = row_tiles_bound(p.slots, p.experts, FEW_SHIFT) * ((p.n + 63) / 64);
   if (wgs < 256) return launch_few_as<1, 4, 4, LW>(p, s);
+  if (wgs < 512) return launch_few_as<1, 2, 4, LW>(p, s);
   if (p.slots / p.experts >= 6 && wgs >= 2048) return launch_few_as<2, 1, 4, LW>(p, s);
   return launch_few_as<1, 1, 8, LW>(p, s);
 }
