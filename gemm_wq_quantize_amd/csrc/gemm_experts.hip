@@ -24,13 +24,14 @@ typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 //
 // Bound by the weights' bytes (369 MB of 64 experts, k = 4096, n = 2816, 256 rows:
 // 81 us, 4.6 TB/s; a bare stream of them 57 to 72).  A workgroup takes a tile of
-// up to 16 rows and 64 CB columns.  The rows sit in LDS, a slab of k at a time, so what flows
-// through the vector memory path is the packed weights alone: each of the four
-// waves streams 16 CB columns over all of k (or KS of them the same ones, a part
-// of k each) from memory straight into registers, DEPTH chunks ahead (a chunk is 32 LW k: 16 LW bytes of each
-// column).  Products on v_mfma_f32_16x16x32_bf16: lane l holds 8 LW consecutive k
-// of column l % 16 (LW packed words) and reads the same k of row l % 16, so slot
-// k of MFMA w is k = chunk + 8 LW (l / 16) + 8 w + (0..7) on both sides.
+// up to 16 rows and 64 CB columns.  The rows sit in LDS, a slab of k at a time,
+// so what flows through the vector memory path is the packed weights alone:
+// each of the four waves streams 16 CB columns over all of k (or KS of them the
+// same ones, a part of k each) from memory straight into registers, DEPTH chunks
+// ahead (a chunk is 32 LW k: 16 LW bytes of each column).  Products on
+// v_mfma_f32_16x16x32_bf16: lane l holds 8 LW consecutive k of column l % 16 (LW
+// packed words) and reads the same k of row l % 16, so slot k of MFMA w is
+// k = chunk + 8 LW (l / 16) + 8 w + (0..7) on both sides.
 //
 // The codes enter the MFMA as 128 + q, exact in bf16, and a chunk lies in one
 // group, so

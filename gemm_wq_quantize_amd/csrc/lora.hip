@@ -151,7 +151,7 @@ constexpr int expand_depth() {
   return MB * (int)sizeof(T) / 2 * 4 + (RS < 2 ? 1 : RS) * 8 <= 24 ? 4 : 2;
 }
 
-template <typename T, int MB, int RS, bool STREAM>
+template <typename T, int MB, int RS>
 __global__ __launch_bounds__(256) void k_lora_expand(LArgs p) {
   constexpr int NS = v_parts<T>();
   constexpr int RP = RS == 0 ? 16 : RS * 32;       // slots of a part
@@ -275,7 +275,7 @@ __global__ __launch_bounds__(256) void k_lora_expand(LArgs p) {
         uint32x4 v[sizeof(w) / 16];
         __builtin_memcpy(v, w, sizeof(w));
 #pragma unroll
-        for (int q = 0; q < (int)sizeof(w) / 16; ++q) store_16<STREAM>(reinterpret_cast<uint8_t*>(dst) + 16 * q, v[q]);
+        for (int q = 0; q < (int)sizeof(w) / 16; ++q) store_16<false>(reinterpret_cast<uint8_t*>(dst) + 16 * q, v[q]);
       } else {
         const T* src = (const T*)p.base + orow[i] * p.n + c0;
 #pragma unroll
@@ -342,8 +342,8 @@ hipError_t shrink(LArgs p, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <typename T, int MB, bool STREAM>
-hipError_t expand_as(LArgs p, hipStream_t s) {
+template <typename T, int MB>
+hipError_t expand(LArgs p, hipStream_t s) {
   const int64_t tiles = row_tiles_bound(p.t, p.adapters + 1, tile_shift<MB>());
   const int64_t blocks = (p.n + 127) / 128;
   // as many columns a workgroup as leave 1024 workgroups: v is made ready once in each
@@ -351,17 +351,11 @@ hipError_t expand_as(LArgs p, hipStream_t s) {
   while (p.col_blocks < 8 && tiles * (blocks / (2 * p.col_blocks)) >= 1024) p.col_blocks *= 2;
   p.tiles_n = (int)((blocks + p.col_blocks - 1) / p.col_blocks);
   const dim3 grid((unsigned)(tiles * p.tiles_n)), wg(256);
-  if (p.rank <= 16) hipLaunchKernelGGL((k_lora_expand<T, MB, 0, STREAM>), grid, wg, 0, s, p);
-  else if (p.rank <= 32) hipLaunchKernelGGL((k_lora_expand<T, MB, 1, STREAM>), grid, wg, 0, s, p);
-  else if (p.rank <= 64) hipLaunchKernelGGL((k_lora_expand<T, MB, 2, STREAM>), grid, wg, 0, s, p);
-  else hipLaunchKernelGGL((k_lora_expand<T, MB, 4, STREAM>), grid, wg, 0, s, p);
+  if (p.rank <= 16) hipLaunchKernelGGL((k_lora_expand<T, MB, 0>), grid, wg, 0, s, p);
+  else if (p.rank <= 32) hipLaunchKernelGGL((k_lora_expand<T, MB, 1>), grid, wg, 0, s, p);
+  else if (p.rank <= 64) hipLaunchKernelGGL((k_lora_expand<T, MB, 2>), grid, wg, 0, s, p);
+  else hipLaunchKernelGGL((k_lora_expand<T, MB, 4>), grid, wg, 0, s, p);
   return hipGetLastError();
-}
-
-template <typename T, int MB>
-hipError_t expand(const LArgs& p, hipStream_t s) {
-  const bool stream = p.t * p.n * (int64_t)sizeof(T) >= kStreamBytes && p.n % 8 == 0;
-  return stream ? expand_as<T, MB, true>(p, s) : expand_as<T, MB, false>(p, s);
 }
 
 }  // namespace

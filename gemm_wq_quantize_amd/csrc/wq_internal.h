@@ -79,14 +79,14 @@ __device__ __forceinline__ void wait_vmcnt() {
 }
 
 // ---- 16-byte stores at the element's own alignment (global accesses need no
-// more on gfx950), optionally non-temporal.  An output beyond the L2s (32 MiB
-// over the XCDs) is not read back from them, and streaming it past them leaves
-// them to the inputs: rows moved there and back (755 MB) 166 -> 142 us, their
-// gradient (873 MB) 180 -> 170, adapters of a prompt (42 MB out) 78 -> 57.  A
-// smaller one is left in L2 for the kernel that reads it next.
+// more on gfx950), optionally non-temporal: for an output beyond the 256 MiB
+// Infinity Cache, which no reader finds there.  Rows dispatched and combined: 335
+// MB of them 166 -> 142 us, whether the same rows are combined or others; at 84
+// MB 46 -> 38 for others, but 33 -> 38 for the same ones, so smaller outputs
+// are stored plainly.
 typedef uint32_t uint32x4_unaligned __attribute__((ext_vector_type(4), aligned(2)));
 typedef uint32_t uint32x4 __attribute__((ext_vector_type(4)));
-constexpr int64_t kStreamBytes = int64_t(32) << 20;
+constexpr int64_t kStreamBytes = int64_t(256) << 20;
 
 // STREAM is a template argument because a branch between the two stores is folded
 // into the plain one.
