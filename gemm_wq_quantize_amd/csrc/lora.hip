@@ -309,16 +309,16 @@ __global__ __launch_bounds__(256) void k_lora_expand(LArgs p) {
 // Rows of a tile.  The first launch reads all of an adapter's A for every tile
 // (from L2), the second all of its B: larger tiles where there are rows to fill
 // them.  Whole calls at rank 64, k = n = 5120, ten requests: first launch with
-// 16, 32, 64 rows 18.3, 19.4, 22.0 us at 512 rows, 67.4, 57.9, 57.5 at 4096 and
-// 242, 208, 186 at 16384; second launch with 16, 32 rows 25.6, 28.8 at 1024, 55.1,
-// 55.3 at 4096 (n = 17280: 123, 112) and 224, 201 at 16384.
+// 16, 32, 64 rows 17.2, 18.2, 19.9 us at 512 rows, 26.3, 23.6, 25.6 at 1024 and
+// 123, 116, 104 at 8192; second launch with 16, 32 rows 23.6, 26.2 at 1024, 59.1,
+// 55.5 at 4096 (n = 17280: 126, 113) and 230, 208 at 16384.
 int shrink_shift(int64_t t) { return t >= 8192 ? 6 : t >= 1024 ? 5 : 4; }
 int expand_shift(int64_t t) { return t >= 4096 ? 5 : 4; }
 
 // k parts: enough workgroups to fill the card where row tiles alone do not, each
 // part at least 256 k, so that every wave has two chunks or more.  More parts
-// are more sums to join: 256 workgroups, 512 with 64-row tiles (512 and 256 at
-// 2048 rows 40.9 and 37.2 us, at 16384 rows 186 and 202).
+// are more sums to join: 256 workgroups, 512 with 64-row tiles (at 1024 rows 26.2
+// us with 256, 27.7 with 512; at 16384 rows 202 and 186).
 int lora_parts(int64_t t, int64_t adapters, int64_t rank, int64_t k) {
   const int64_t wgs = row_tiles_bound(t, adapters, shrink_shift(t)) * ((rank + 63) / 64);
   const int64_t want = shrink_shift(t) == 6 ? 512 : 256;
