@@ -129,10 +129,13 @@ __global__ __launch_bounds__(256) void k_lora_shrink(LArgs p) {
 
 // --------------------------------------------------- out = base + scale B v
 //
-// B's rows are the first MFMA operand, v's rows the second, so a lane's results
-// are neighbouring columns of one row: blocks 0 and 1 of 32 columns take
-// columns 8 (i / 4) + i % 4 and 4 more, and a lane then holds 8 in a row --
-// one 16-byte access of base and out.  The MFMA takes bf16, so v enters as a
+// Four neighbouring lanes load and store 64 bytes in a row, of B, of base and of
+// out: a load whose neighbouring lanes lie in 16 different rows, as the MFMA's
+// operands do, reaches 37 B/ns a CU from L2 where one of whole lines reaches 120.
+// B's blocks and the results therefore change places in LDS, in a region that each
+// wave has to itself.  B's rows are the first MFMA operand, v's rows the second,
+// so a lane's results are neighbouring columns of one row: blocks 0 and 1 of 32
+// columns take columns 8 (i / 4) + i % 4 and 4 more, and a lane holds 8 in a row.  The MFMA takes bf16, so v enters as a
 // sum of bf16 parts: two (17 bits) where out is bf16, three (all of float32's
 // 24) where it is float32; they fill MFMA slots that a small rank leaves
 // empty.  RS is the number of 32-slot steps a part takes; 0: rank <= 16, two
@@ -144,6 +147,12 @@ template <typename T> constexpr int v_parts() { return sizeof(T) == 2 ? 2 : 3; }
 template <typename T> struct Eight;
 template <> struct Eight<__bf16> { struct alignas(2) raw { uint16_t h[8]; }; };
 template <> struct Eight<float> { struct alignas(4) raw { float f[8]; }; };
+
+// the order of a wave's accesses to LDS that no other wave touches
+__device__ __forceinline__ void wave_order() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
 
 // ring depth: 64 registers of operands or a little more
 template <typename T, int MB, int RS>
@@ -157,9 +166,13 @@ __global__ __launch_bounds__(256) void k_lora_expand(LArgs p) {
   constexpr int RP = RS == 0 ? 16 : RS * 32;       // slots of a part
   constexpr int STEPS = (NS * RP + 31) / 32;
   constexpr int NB = RS == 0 ? 1 : RS;             // steps with a B operand of their own: the parts share them
-  constexpr int PITCH = STEPS * 32 + 8;            // bf16 per LDS row; 16 bytes off a power of two
+  constexpr int PITCH = STEPS * 32 + 8;            // bf16 per row of v; 16 bytes off a power of two
+  constexpr int BL = RP / 16;                      // 16-byte pieces of 32 columns of B a lane loads
+  constexpr int B_PITCH = RP + 8, O_PITCH = 36;    // bf16 per column of B, floats per row of results
+  constexpr int B_BYTES = 32 * B_PITCH * 2, O_BYTES = MB * 16 * O_PITCH * 4;
   typedef typename Eight<T>::raw raw_t;
   __shared__ __attribute__((aligned(16))) uint16_t vs[MB * 16 * PITCH];
+  __shared__ __attribute__((aligned(16))) uint8_t own[4][B_BYTES > O_BYTES ? B_BYTES : O_BYTES];  // per wave
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int m = (int)(blockIdx.x / (unsigned)p.tiles_n), tn = (int)(blockIdx.x % (unsigned)p.tiles_n);
@@ -171,30 +184,31 @@ __global__ __launch_bounds__(256) void k_lora_expand(LArgs p) {
 
   const int lr = lane & 15, lq = lane >> 4;
   const uint16_t* bl = p.b + (int64_t)(live ? t.bin : 0) * p.n * p.rank;
+  uint16_t* bs = reinterpret_cast<uint16_t*>(own[wave]);
+  float* os = reinterpret_cast<float*>(own[wave]);
   // a ring of DEPTH 32-column blocks: B's and base's loads of the next ones are in
-  // flight while one is multiplied.  Columns past n and rows past the tile's last
-  // load another one's and store nothing.
+  // flight while one is multiplied.  Pieces past B's last and rows past the
+  // tile's last load another one's and store nothing.
   constexpr int DEPTH = expand_depth<T, MB, RS>();
-  bf16x8 bf[DEPTH][NB][2];
+  u32x4 braw[DEPTH][BL];
   raw_t base[DEPTH][MB];
   const bool with_base = p.base && p.n >= 8;
-  int64_t orow[MB];   // a lane's rows, -1 where there is none
+  int64_t orow[MB];   // a lane's rows of base and out, -1 where there is none
   const T* brow[MB];  // base of a row that exists
+  int b_to[BL];       // where a lane's pieces of B go in LDS, -1: nowhere
+#pragma unroll
+  for (int i = 0; i < BL; ++i) {
+    const int q = lane + 64 * i, per = p.rank / 8;
+    b_to[i] = q < 32 * per ? q / per * B_PITCH + q % per * 8 : -1;
+  }
   auto block_col = [&](int cb) { return ((int64_t)tn * p.col_blocks + cb) * 128 + wave * 32; };
   auto load_b = [&](int cb, int d) {
-    const int64_t n0 = block_col(cb);
+    const int64_t at = block_col(cb) * p.rank + lane * 8, last = p.n * p.rank - 8;
 #pragma unroll
-    for (int s = 0; s < NB; ++s) {
-      const int r = min((s * 32 + lq * 8) % RP, p.rank - 8);  // slots past the rank meet a zero of v
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int64_t col = min(n0 + (lr >> 2) * 8 + h * 4 + (lr & 3), p.n - 1);
-        bf[d][s][h] = *reinterpret_cast<const bf16x8*>(bl + col * p.rank + r);
-      }
-    }
+    for (int i = 0; i < BL; ++i) braw[d][i] = *reinterpret_cast<const u32x4*>(bl + min(at + 512 * i, last));
   };
   auto load_base = [&](int cb, int d) {
-    const int64_t c0 = min(block_col(cb) + lq * 8, p.n - 8);
+    const int64_t c0 = min(block_col(cb) + (lane & 3) * 8, p.n - 8);
 #pragma unroll
     for (int i = 0; i < MB; ++i) base[d][i] = *reinterpret_cast<const raw_t*>(brow[i] + c0);
   };
@@ -206,8 +220,9 @@ __global__ __launch_bounds__(256) void k_lora_expand(LArgs p) {
       if (d < blocks) load_b(d, d);
 #pragma unroll
   for (int i = 0; i < MB; ++i) {
-    const int64_t r = x_row(p, t.row0 + min(i * 16 + lr, t.rows - 1));
-    orow[i] = i * 16 + lr < t.rows ? r : -1;
+    const int row = i * 16 + (lane >> 2);
+    const int64_t r = x_row(p, t.row0 + min(row, t.rows - 1));
+    orow[i] = row < t.rows ? r : -1;
     brow[i] = (const T*)p.base + max(r, (int64_t)0) * p.n;
   }
   if (with_base)
@@ -243,10 +258,24 @@ __global__ __launch_bounds__(256) void k_lora_expand(LArgs p) {
     __syncthreads();
   }
   auto block = [&](int cb, int d) {
-    floatx4 acc[MB][2];
-#pragma unroll
-    for (int i = 0; i < MB; ++i) acc[i][0] = acc[i][1] = floatx4{0.f, 0.f, 0.f, 0.f};
     if (live) {
+      // B to LDS and back as operands; results the same way.  A wave's LDS accesses
+      // run in order, so its own region needs no barrier, only the compiler's order.
+#pragma unroll
+      for (int i = 0; i < BL; ++i)
+        if (b_to[i] >= 0) *reinterpret_cast<u32x4*>(bs + b_to[i]) = braw[d][i];
+      wave_order();
+      bf16x8 bf[NB][2];
+#pragma unroll
+      for (int s = 0; s < NB; ++s) {
+        const int r = min((s * 32 + lq * 8) % RP, p.rank - 8);  // slots past the rank meet a zero of v
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          bf[s][h] = *reinterpret_cast<const bf16x8*>(bs + ((lr >> 2) * 8 + h * 4 + (lr & 3)) * B_PITCH + r);
+      }
+      floatx4 acc[MB][2];
+#pragma unroll
+      for (int i = 0; i < MB; ++i) acc[i][0] = acc[i][1] = floatx4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int s = 0; s < STEPS; ++s)
 #pragma unroll
@@ -254,20 +283,29 @@ __global__ __launch_bounds__(256) void k_lora_expand(LArgs p) {
           const bf16x8 vf = *reinterpret_cast<const bf16x8*>(vs + (i * 16 + lr) * PITCH + s * 32 + lq * 8);
 #pragma unroll
           for (int h = 0; h < 2; ++h)
-            acc[i][h] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bf[d][s % NB][h], vf, acc[i][h], 0, 0, 0);
+            acc[i][h] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bf[s % NB][h], vf, acc[i][h], 0, 0, 0);
         }
+      wave_order();
+#pragma unroll
+      for (int i = 0; i < MB; ++i)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          *reinterpret_cast<floatx4*>(os + (i * 16 + lr) * O_PITCH + lq * 8 + h * 4) = acc[i][h];
+      wave_order();
     }
-    const int64_t c0 = block_col(cb) + lq * 8;
+    const int64_t c0 = block_col(cb) + (lane & 3) * 8;
 #pragma unroll
     for (int i = 0; i < MB; ++i) {
+      floatx4 f[2] = {floatx4{0.f, 0.f, 0.f, 0.f}, floatx4{0.f, 0.f, 0.f, 0.f}};
+      if (live)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          f[h] = *reinterpret_cast<const floatx4*>(os + (i * 16 + (lane >> 2)) * O_PITCH + (lane & 3) * 8 + h * 4);
       T w[8];
       if (with_base) __builtin_memcpy(w, &base[d][i], sizeof(w));
       if (live || !with_base) {  // a row without an adapter keeps base's bits
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float f = acc[i][e >> 2][e & 3];
-          w[e] = (T)(with_base ? f + (float)w[e] : f);
-        }
+        for (int e = 0; e < 8; ++e) w[e] = (T)(with_base ? f[e >> 2][e & 3] + (float)w[e] : f[e >> 2][e & 3]);
       }
       if (orow[i] < 0 || c0 >= p.n) continue;
       T* dst = (T*)p.out + orow[i] * p.n + c0;
@@ -280,11 +318,12 @@ __global__ __launch_bounds__(256) void k_lora_expand(LArgs p) {
         const T* src = (const T*)p.base + orow[i] * p.n + c0;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          const float f = acc[i][e >> 2][e & 3];
-          if (c0 + e < p.n) dst[e] = !p.base ? (T)f : live ? (T)(f + (float)src[e]) : src[e];
+          const float x = f[e >> 2][e & 3];
+          if (c0 + e < p.n) dst[e] = !p.base ? (T)x : live ? (T)(x + (float)src[e]) : src[e];
         }
       }
     }
+    wave_order();
   };
   int cb = 0;
   for (; cb + 2 * DEPTH <= blocks; cb += DEPTH)
