@@ -41,16 +41,26 @@ __device__ __forceinline__ int64_t x_row(const LArgs& p, int i) {
 // ------------------------------------------------------------ v = A x
 //
 // A workgroup takes MB blocks of 16 rows, NR blocks of 16 ranks and one part of
-// k; its four waves take a quarter of that each and join in LDS.  Operands go
-// from memory to v_mfma_f32_16x16x32_bf16 as they lie, DEPTH 32-k chunks ahead:
-// 16 bytes of a row are a lane's 8 slots.  Rows and ranks past the last repeat
-// it.
+// k; its four waves take a quarter of that each and join in LDS.  A wave loads
+// 64-k chunks of its rows and ranks, whole 128-byte lines by eight neighbouring
+// lanes, DEPTH chunks ahead, and turns them into operands of
+// v_mfma_f32_16x16x32_bf16 in an LDS region of its own.  Rows and ranks past the
+// last repeat it.
 template <int MB> constexpr int tile_shift() { return MB == 1 ? 4 : MB == 2 ? 5 : 6; }
+
+// the order of a wave's accesses to LDS that no other wave touches
+__device__ __forceinline__ void wave_order() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
 
 template <int MB, int NR>
 __global__ __launch_bounds__(256) void k_lora_shrink(LArgs p) {
-  constexpr int DEPTH = MB + NR <= 3 ? 8 : MB + NR <= 6 ? 4 : 2;
-  __shared__ __attribute__((aligned(16))) float part[4][MB * NR * 4][64];
+  constexpr int DEPTH = MB + NR <= 3 ? 4 : 2;
+  constexpr int PITCH = 72;                          // bf16 per LDS row of 64 k: 16 bytes off a multiple of 128
+  constexpr int OWN = (MB + NR) * 16 * PITCH * 2;    // a wave's region
+  constexpr int JOIN = MB * NR * 4 * 64 * 4;         // a wave's sums
+  __shared__ __attribute__((aligned(16))) uint8_t smem[4 * (OWN > JOIN ? OWN : JOIN)];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   unsigned id = blockIdx.x;
@@ -61,37 +71,72 @@ __global__ __launch_bounds__(256) void k_lora_shrink(LArgs p) {
   int count;
   if (!find_row_tile<false>(p.offsets, p.adapters, p.t, tile_shift<MB>(), m, t, count)) return;
 
-  const int lr = lane & 15, lq = lane >> 4;
-  const int nch = (int)(p.k / 32);
+  const int nch = (int)((p.k + 63) / 64);
   // this wave's chunks: the parts' waves in the order of k
   const int slot = part_k * 4 + wave, slots = p.parts * 4;
   const int c0 = (int)((int64_t)nch * slot / slots), cnt = (int)((int64_t)nch * (slot + 1) / slots) - c0;
-  const uint16_t* xr[MB];
-  const uint16_t* ar[NR];
+  const int sub = lane >> 3, piece = lane & 7;       // load j of a block: row 8 j + sub, 16 bytes `piece`
+  const uint16_t* xr[MB][2];
+  const uint16_t* ar[NR][2];
 #pragma unroll
   for (int j = 0; j < NR; ++j)
-    ar[j] = p.a + ((int64_t)t.bin * p.rank + min(rg * (NR * 16) + j * 16 + lr, p.rank - 1)) * p.k + c0 * 32 + lq * 8;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      ar[j][h] = p.a + ((int64_t)t.bin * p.rank + min(rg * (NR * 16) + j * 16 + h * 8 + sub, p.rank - 1)) * p.k;
 #pragma unroll
   for (int i = 0; i < MB; ++i)
-    xr[i] = p.x + max(x_row(p, t.row0 + min(i * 16 + lr, t.rows - 1)), (int64_t)0) * p.k + c0 * 32 + lq * 8;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      xr[i][h] = p.x + max(x_row(p, t.row0 + min(i * 16 + h * 8 + sub, t.rows - 1)), (int64_t)0) * p.k;
   floatx4 acc[MB][NR];
 #pragma unroll
   for (int i = 0; i < MB; ++i)
 #pragma unroll
     for (int j = 0; j < NR; ++j) acc[i][j] = floatx4{0.f, 0.f, 0.f, 0.f};
-  bf16x8 xf[DEPTH][MB], af[DEPTH][NR];
+  u32x4 xf[DEPTH][MB][2], af[DEPTH][NR][2];
   auto load = [&](int ch, int d) {
+    // the second half of the last chunk may lie past k: x there counts as zero
+    const int64_t at = min((int64_t)(c0 + ch) * 64 + piece * 8, p.k - 8);
 #pragma unroll
-    for (int j = 0; j < NR; ++j) af[d][j] = *reinterpret_cast<const bf16x8*>(ar[j] + (int64_t)ch * 32);
+    for (int j = 0; j < NR; ++j)
 #pragma unroll
-    for (int i = 0; i < MB; ++i) xf[d][i] = *reinterpret_cast<const bf16x8*>(xr[i] + (int64_t)ch * 32);
-  };
-  auto fold = [&](int d) {
+      for (int h = 0; h < 2; ++h) af[d][j][h] = *reinterpret_cast<const u32x4*>(ar[j][h] + at);
 #pragma unroll
     for (int i = 0; i < MB; ++i)
 #pragma unroll
+      for (int h = 0; h < 2; ++h) xf[d][i][h] = *reinterpret_cast<const u32x4*>(xr[i][h] + at);
+  };
+  uint16_t* own = reinterpret_cast<uint16_t*>(smem + wave * OWN);
+  const int lr = lane & 15, lq = lane >> 4;
+  auto fold = [&](int ch, int d) {
+    const bool past = (int64_t)(c0 + ch) * 64 + piece * 8 >= p.k;
+#pragma unroll
+    for (int i = 0; i < MB; ++i)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        *reinterpret_cast<u32x4*>(own + (i * 16 + h * 8 + sub) * PITCH + piece * 8) =
+            past ? u32x4{0, 0, 0, 0} : xf[d][i][h];
+#pragma unroll
+    for (int j = 0; j < NR; ++j)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        *reinterpret_cast<u32x4*>(own + ((MB + j) * 16 + h * 8 + sub) * PITCH + piece * 8) = af[d][j][h];
+    wave_order();
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      bf16x8 a[NR];
+#pragma unroll
       for (int j = 0; j < NR; ++j)
-        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf[d][i], af[d][j], acc[i][j], 0, 0, 0);
+        a[j] = *reinterpret_cast<const bf16x8*>(own + ((MB + j) * 16 + lr) * PITCH + s * 32 + lq * 8);
+#pragma unroll
+      for (int i = 0; i < MB; ++i) {
+        const bf16x8 x = *reinterpret_cast<const bf16x8*>(own + (i * 16 + lr) * PITCH + s * 32 + lq * 8);
+#pragma unroll
+        for (int j = 0; j < NR; ++j)
+          acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, a[j], acc[i][j], 0, 0, 0);
+      }
+    }
+    wave_order();
   };
 #pragma unroll
   for (int d = 0; d < DEPTH; ++d)
@@ -100,15 +145,17 @@ __global__ __launch_bounds__(256) void k_lora_shrink(LArgs p) {
   for (; ch + 2 * DEPTH <= cnt; ch += DEPTH)
 #pragma unroll
     for (int d = 0; d < DEPTH; ++d) {
-      fold(d);
+      fold(ch + d, d);
       load(ch + d + DEPTH, d);
     }
   for (; ch < cnt; ch += DEPTH)
 #pragma unroll
     for (int d = 0; d < DEPTH; ++d) {
-      if (ch + d < cnt) fold(d);
+      if (ch + d < cnt) fold(ch + d, d);
       if (ch + d + DEPTH < cnt) load(ch + d + DEPTH, d);
     }
+  __syncthreads();  // the sums take the waves' regions
+  float(*part)[MB * NR * 4][64] = reinterpret_cast<float(*)[MB * NR * 4][64]>(smem);
 #pragma unroll
   for (int i = 0; i < MB; ++i)
 #pragma unroll
@@ -147,12 +194,6 @@ template <typename T> constexpr int v_parts() { return sizeof(T) == 2 ? 2 : 3; }
 template <typename T> struct Eight;
 template <> struct Eight<__bf16> { struct alignas(2) raw { uint16_t h[8]; }; };
 template <> struct Eight<float> { struct alignas(4) raw { float f[8]; }; };
-
-// the order of a wave's accesses to LDS that no other wave touches
-__device__ __forceinline__ void wave_order() {
-  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-  __builtin_amdgcn_wave_barrier();
-}
 
 // ring depth: 64 registers of operands or a little more
 template <typename T, int MB, int RS>
