@@ -46,7 +46,7 @@ __device__ __forceinline__ int64_t x_row(const LArgs& p, int i) {
 // lanes, DEPTH chunks ahead, and turns them into operands of
 // v_mfma_f32_16x16x32_bf16 in an LDS region of its own.  Rows and ranks past the
 // last repeat it.
-template <int MB> constexpr int tile_shift() { return MB == 1 ? 4 : MB == 2 ? 5 : 6; }
+template <int MB> constexpr int tile_shift() { return MB == 1 ? 4 : 5; }
 
 // the order of a wave's accesses to LDS that no other wave touches
 __device__ __forceinline__ void wave_order() {
@@ -388,20 +388,20 @@ __global__ __launch_bounds__(256) void k_lora_expand(LArgs p) {
 
 // Rows of a tile.  The first launch reads all of an adapter's A for every tile
 // (from L2), the second all of its B: larger tiles where there are rows to fill
-// them.  Whole calls at rank 64, k = n = 5120, ten requests: first launch with
-// 16, 32, 64 rows 17.2, 18.2, 19.9 us at 512 rows, 26.3, 23.6, 25.6 at 1024 and
-// 123, 116, 104 at 8192; second launch with 16, 32 rows 23.6, 26.2 at 1024, 59.1,
-// 55.5 at 4096 (n = 17280: 126, 113) and 230, 208 at 16384.
-int shrink_shift(int64_t t) { return t >= 8192 ? 6 : t >= 1024 ? 5 : 4; }
-int expand_shift(int64_t t) { return t >= 4096 ? 5 : 4; }
+// them.  Whole calls at rank 64, k = n = 5120, ten requests: first launch with 16,
+// 32 rows 21.6, 23.5 us at 1024 rows, 51.4, 46.9 at 4096 and 175, 163 at 16384 (64
+// rows: 164); second launch with 16, 32 rows 46.8, 47.7 at 4096, 84.5, 83.1 at 8192
+// and 163, 155 at 16384.
+int shrink_shift(int64_t t) { return t >= 4096 ? 5 : 4; }
+int expand_shift(int64_t t) { return t >= 8192 ? 5 : 4; }
 
 // k parts: enough workgroups to fill the card where row tiles alone do not, each
-// part at least 256 k, so that every wave has two chunks or more.  More parts
-// are more sums to join: 256 workgroups, 512 with 64-row tiles (at 1024 rows 26.2
-// us with 256, 27.7 with 512; at 16384 rows 202 and 186).
+// part at least 256 k, so that every wave has a chunk or more.  More parts are
+// more sums to join: 256 workgroups, 512 with 32-row tiles (at 1024 rows 21.6 us
+// with 256, 23.7 with 512; at 8192 rows 84.5 and 79.1).
 int lora_parts(int64_t t, int64_t adapters, int64_t rank, int64_t k) {
   const int64_t wgs = row_tiles_bound(t, adapters, shrink_shift(t)) * ((rank + 63) / 64);
-  const int64_t want = shrink_shift(t) == 6 ? 512 : 256;
+  const int64_t want = shrink_shift(t) == 5 ? 512 : 256;
   int64_t parts = wgs > 0 ? (want - 1 + wgs) / wgs : 1;
   if (parts > k / 256) parts = k / 256;
   if (parts > 16) parts = 16;
@@ -464,9 +464,9 @@ hipError_t launch_lora(const uint16_t* x, int64_t t, int64_t k, const int32_t* o
   p.rank = (int)rank;
   p.rank_pad = pad16(rank);
   p.parts = lora_parts(t, adapters, rank, k);
-  const int sh = shrink_shift(t), ex = expand_shift(t);
-  const hipError_t e = sh == 6 ? shrink<4>(p, s) : sh == 5 ? shrink<2>(p, s) : shrink<1>(p, s);
+  const hipError_t e = shrink_shift(t) == 5 ? shrink<2>(p, s) : shrink<1>(p, s);
   if (e != hipSuccess) return e;
+  const int ex = expand_shift(t);
   if (out_bf16) return ex == 5 ? expand<__bf16, 2>(p, s) : expand<__bf16, 1>(p, s);
   return ex == 5 ? expand<float, 2>(p, s) : expand<float, 1>(p, s);
 }

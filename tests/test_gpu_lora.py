@@ -61,7 +61,8 @@ def check(c, ids, dt):
 
 SIZES = [(1, 32, 1, 1, 8), (1, 4096, 5120, 64, 16), (7, 96, 33, 3, 24), (33, 512, 260, 40, 16), (64, 1024, 1000, 2, 64),
          (100, 320, 127, 5, 128), (40, 2560, 136, 600, 32), (1025, 256, 257, 3, 8), (1500, 512, 384, 30, 64),
-         (2000, 288, 200, 1000, 40), (1100, 608, 130, 2, 104)]
+         (2000, 288, 200, 1000, 40), (1100, 608, 130, 2, 104),
+         (4100, 96, 100, 5, 24), (8200, 160, 72, 40, 128)]
 
 
 @pytest.mark.parametrize("t,k,n,adapters,rank", SIZES)
