@@ -31,6 +31,9 @@ int dtype_size(int dt) { return dt == WQ_F32 ? 4 : 2; }
 
 int hip_status(hipError_t e) { return e == hipSuccess ? WQ_OK : WQ_EHIP; }
 
+// of the launches that refuse more workgroups than one holds before they enqueue
+int grid_status(hipError_t e) { return e == hipErrorInvalidConfiguration ? WQ_ESHAPE : hip_status(e); }
+
 hipStream_t as_stream(void* s) { return reinterpret_cast<hipStream_t>(s); }
 
 
@@ -114,8 +117,7 @@ bool valid_dtype(int dt) { return dt == WQ_F32 || dt == WQ_F16 || dt == WQ_BF16;
 
 // sizes shared by the calls that move rows: false if refused
 bool valid_rows(int64_t t, int64_t topk, int64_t h) {
-  return mul_sat(t, topk) <= wq::kMaxSlots && h < (int64_t(1) << 31) &&
-         mul_sat(t, h / 1024 + 1) <= kMaxGrid;  // at least 1024 elements a workgroup, or whole rows
+  return mul_sat(t, topk) <= wq::kMaxSlots && h < (int64_t(1) << 31);
 }
 }  // namespace
 
@@ -301,7 +303,7 @@ int wq_dispatch_rows(const void* x, int dtype, const int32_t* place, int64_t t, 
   if (!valid_rows(t, topk, h)) return WQ_ESHAPE;
   const uintptr_t es = (uintptr_t)dtype_size(dtype);
   if (!aligned(x, es) || !aligned(out, es) || !aligned(place, 4)) return WQ_EALIGN;
-  return hip_status(wq::launch_dispatch_rows(x, dtype, place, t, topk, h, out, as_stream(stream)));
+  return grid_status(wq::launch_dispatch_rows(x, dtype, place, t, topk, h, out, as_stream(stream)));
 }
 
 int wq_combine_rows(const void* rows, int dtype, const int32_t* place, const float* weights, int64_t t, int64_t topk,
@@ -313,7 +315,7 @@ int wq_combine_rows(const void* rows, int dtype, const int32_t* place, const flo
   if (!valid_rows(t, topk, h)) return WQ_ESHAPE;
   const uintptr_t es = (uintptr_t)dtype_size(dtype);
   if (!aligned(rows, es) || !aligned(out, es) || !aligned(place, 4) || !aligned(weights, 4)) return WQ_EALIGN;
-  return hip_status(wq::launch_combine_rows(rows, dtype, place, weights, t, topk, h, out, as_stream(stream)));
+  return grid_status(wq::launch_combine_rows(rows, dtype, place, weights, t, topk, h, out, as_stream(stream)));
 }
 
 int wq_combine_rows_grad(const void* d_out, const void* rows, int dtype, const int32_t* place, const float* weights,
@@ -327,7 +329,7 @@ int wq_combine_rows_grad(const void* d_out, const void* rows, int dtype, const i
   if (!aligned(d_out, es) || !aligned(rows, es) || !aligned(d_rows, es) || !aligned(place, 4) ||
       !aligned(weights, 4) || !aligned(d_weights, 4))
     return WQ_EALIGN;
-  return hip_status(wq::launch_combine_rows_grad(d_out, rows, dtype, place, weights, t, topk, h, d_rows, d_weights,
+  return grid_status(wq::launch_combine_rows_grad(d_out, rows, dtype, place, weights, t, topk, h, d_rows, d_weights,
                                                  as_stream(stream)));
 }
 
@@ -345,13 +347,12 @@ int wq_gemm_w4a16_experts(const uint16_t* a, int64_t a_rows, const int32_t* orde
   if (order ? topk < 1 || mul_sat(a_rows, topk) != slots : a_rows != slots) return WQ_ESHAPE;
   if (mul_sat(n, experts) >= (int64_t(1) << 31)) return WQ_ESHAPE;
   if (order && mul_sat(a_rows, 2 * k) >= (int64_t(1) << 31)) return WQ_ESHAPE;  // 32-bit offsets of the gather
-  if (mul_sat(wq::row_tiles_bound(slots, experts, 4), n / 16 + 1) > kMaxGrid) return WQ_ESHAPE;
   if (group < 64) return WQ_EUNSUPPORTED;  // a 64-k step must lie in one group
   if (layout != WQ_LAYOUT_GFX950) return WQ_EUNSUPPORTED;
   if (!aligned(a, 16) || !aligned(b, 16) || !aligned(c_out, 16) || !aligned(scales, 4) || !aligned(zeros, 4) ||
       !aligned(order, 4) || !aligned(offsets, 4))
     return WQ_EALIGN;
-  return hip_status(wq::launch_gemm_w4a16_experts(a, a_rows, order, topk, offsets, slots, experts, b, scales, zeros,
+  return grid_status(wq::launch_gemm_w4a16_experts(a, a_rows, order, topk, offsets, slots, experts, b, scales, zeros,
                                                   group, zero_const, n, k, c_out, as_stream(stream)));
 }
 
@@ -372,13 +373,12 @@ int wq_lora(const uint16_t* x, int64_t t, int64_t k, const int32_t* order, const
   if (t == 0 || n == 0) return WQ_OK;
   if (!x || !order || !offsets || !a || !b || !scales || !out || !workspace) return WQ_EINVAL;
   if (workspace_bytes < need) return WQ_EINVAL;
-  if (n >= (int64_t(1) << 31) || mul_sat(wq::row_tiles_bound(t, adapters + 1, 4), n / 128 + 1) > kMaxGrid)
-    return WQ_ESHAPE;
+  if (n >= (int64_t(1) << 31)) return WQ_ESHAPE;
   const uintptr_t es = (uintptr_t)dtype_size(out_dtype);
   if (!aligned(x, 16) || !aligned(a, 16) || !aligned(b, 16) || !aligned(workspace, 16) || !aligned(order, 4) ||
       !aligned(offsets, 4) || !aligned(scales, 4) || !aligned(base, es) || !aligned(out, es))
     return WQ_EALIGN;
-  return hip_status(wq::launch_lora(x, t, k, order, offsets, adapters, a, b, rank, scales, base, out,
+  return grid_status(wq::launch_lora(x, t, k, order, offsets, adapters, a, b, rank, scales, base, out,
                                     out_dtype == WQ_BF16, n, workspace, as_stream(stream)));
 }
 

@@ -235,7 +235,9 @@ __global__ __launch_bounds__(256) void k_experts_few(EArgs p) {
 template <int CB, int KS, int DEPTH, int LW>
 hipError_t launch_few_as(EArgs p, hipStream_t s) {
   p.tiles_n = (int)((p.n + few_cols<CB, KS>() - 1) / few_cols<CB, KS>());
-  const dim3 grid((unsigned)(row_tiles_bound(p.slots, p.experts, FEW_SHIFT) * p.tiles_n));
+  const int64_t groups = row_tiles_bound(p.slots, p.experts, FEW_SHIFT) * p.tiles_n;
+  if (groups > kMaxGroups) return hipErrorInvalidConfiguration;
+  const dim3 grid((unsigned)groups);
   if (p.zeros) hipLaunchKernelGGL((k_experts_few<CB, KS, DEPTH, LW, true>), grid, dim3(256), 0, s, p);
   else hipLaunchKernelGGL((k_experts_few<CB, KS, DEPTH, LW, false>), grid, dim3(256), 0, s, p);
   return hipGetLastError();
@@ -532,7 +534,9 @@ __global__ __launch_bounds__(256, 2) void k_experts_tiles(EArgs p) {
 
 hipError_t launch_tiles(EArgs p, hipStream_t s) {
   p.tiles_n = (int)((p.n + TN - 1) / TN);
-  const dim3 grid((unsigned)(row_tiles_bound(p.slots, p.experts, TILE_SHIFT) * p.tiles_n)), wg(256);
+  const int64_t groups = row_tiles_bound(p.slots, p.experts, TILE_SHIFT) * p.tiles_n;
+  if (groups > kMaxGroups) return hipErrorInvalidConfiguration;
+  const dim3 grid((unsigned)groups), wg(256);
   // the fp16-magic unpacking needs a zero that is a multiple of 2^-5 below 1024
   const float zs = p.zero_const * 32.f;
   const bool mix = std::fabs(p.zero_const) < 1024.f && zs == std::nearbyint(zs);

@@ -410,27 +410,39 @@ int lora_parts(int64_t t, int64_t adapters, int64_t rank, int64_t k) {
 
 int pad16(int64_t rank) { return (int)((rank + 15) / 16 * 16); }
 
-template <int MB>
-hipError_t shrink(LArgs p, hipStream_t s) {
-  const int nr = p.rank <= 16 ? 1 : p.rank <= 32 ? 2 : 4;
+// 16-rank blocks of a workgroup of the first launch
+int shrink_blocks(int64_t rank) { return rank <= 16 ? 1 : rank <= 32 ? 2 : 4; }
+
+// the launches' workgroups, and what divides them
+int64_t shrink_groups(LArgs& p) {
+  const int nr = shrink_blocks(p.rank);
   p.rank_groups = (p.rank + nr * 16 - 1) / (nr * 16);
-  const unsigned grid =
-      (unsigned)(row_tiles_bound(p.t, p.adapters, tile_shift<MB>()) * p.parts * p.rank_groups);
-  if (nr == 1) hipLaunchKernelGGL((k_lora_shrink<MB, 1>), dim3(grid), dim3(256), 0, s, p);
-  else if (nr == 2) hipLaunchKernelGGL((k_lora_shrink<MB, 2>), dim3(grid), dim3(256), 0, s, p);
-  else hipLaunchKernelGGL((k_lora_shrink<MB, 4>), dim3(grid), dim3(256), 0, s, p);
-  return hipGetLastError();
+  return row_tiles_bound(p.t, p.adapters, shrink_shift(p.t)) * p.parts * p.rank_groups;
 }
 
-template <typename T, int MB>
-hipError_t expand(LArgs p, hipStream_t s) {
-  const int64_t tiles = row_tiles_bound(p.t, p.adapters + 1, tile_shift<MB>());
+int64_t expand_groups(LArgs& p) {
+  const int64_t tiles = row_tiles_bound(p.t, p.adapters + 1, expand_shift(p.t));
   const int64_t blocks = (p.n + 127) / 128;
   // as many columns a workgroup as leave 1024 workgroups: v is made ready once in each
   p.col_blocks = 1;
   while (p.col_blocks < 8 && tiles * (blocks / (2 * p.col_blocks)) >= 1024) p.col_blocks *= 2;
   p.tiles_n = (int)((blocks + p.col_blocks - 1) / p.col_blocks);
-  const dim3 grid((unsigned)(tiles * p.tiles_n)), wg(256);
+  return tiles * p.tiles_n;
+}
+
+template <int MB>
+hipError_t shrink(const LArgs& p, unsigned groups, hipStream_t s) {
+  const dim3 grid(groups), wg(256);
+  const int nr = shrink_blocks(p.rank);
+  if (nr == 1) hipLaunchKernelGGL((k_lora_shrink<MB, 1>), grid, wg, 0, s, p);
+  else if (nr == 2) hipLaunchKernelGGL((k_lora_shrink<MB, 2>), grid, wg, 0, s, p);
+  else hipLaunchKernelGGL((k_lora_shrink<MB, 4>), grid, wg, 0, s, p);
+  return hipGetLastError();
+}
+
+template <typename T, int MB>
+hipError_t expand(const LArgs& p, unsigned groups, hipStream_t s) {
+  const dim3 grid(groups), wg(256);
   if (p.rank <= 16) hipLaunchKernelGGL((k_lora_expand<T, MB, 0>), grid, wg, 0, s, p);
   else if (p.rank <= 32) hipLaunchKernelGGL((k_lora_expand<T, MB, 1>), grid, wg, 0, s, p);
   else if (p.rank <= 64) hipLaunchKernelGGL((k_lora_expand<T, MB, 2>), grid, wg, 0, s, p);
@@ -464,11 +476,14 @@ hipError_t launch_lora(const uint16_t* x, int64_t t, int64_t k, const int32_t* o
   p.rank = (int)rank;
   p.rank_pad = pad16(rank);
   p.parts = lora_parts(t, adapters, rank, k);
-  const hipError_t e = shrink_shift(t) == 5 ? shrink<2>(p, s) : shrink<1>(p, s);
+  const int64_t first = shrink_groups(p), second = expand_groups(p);
+  if (first > kMaxGroups || second > kMaxGroups) return hipErrorInvalidConfiguration;
+  const unsigned g1 = (unsigned)first, g2 = (unsigned)second;
+  const hipError_t e = shrink_shift(t) == 5 ? shrink<2>(p, g1, s) : shrink<1>(p, g1, s);
   if (e != hipSuccess) return e;
   const int ex = expand_shift(t);
-  if (out_bf16) return ex == 5 ? expand<__bf16, 2>(p, s) : expand<__bf16, 1>(p, s);
-  return ex == 5 ? expand<float, 2>(p, s) : expand<float, 1>(p, s);
+  if (out_bf16) return ex == 5 ? expand<__bf16, 2>(p, g2, s) : expand<__bf16, 1>(p, g2, s);
+  return ex == 5 ? expand<float, 2>(p, g2, s) : expand<float, 1>(p, g2, s);
 }
 
 }  // namespace wq

@@ -386,18 +386,20 @@ bool streams(int64_t rows, int64_t h) {
 }
 
 template <int DT>
-unsigned move_grid(MoveArgs& p) {
+int64_t move_grid(MoveArgs& p) {
   const int64_t nv = (p.h + per_lane<DT>() - 1) / per_lane<DT>();
   p.lane_bits = 8;
   while (p.lane_bits > 0 && (int64_t(1) << (p.lane_bits - 1)) >= nv) --p.lane_bits;
   p.chunks = (int)((nv + 255) / 256);
   const int per = 256 >> p.lane_bits;
-  return (unsigned)(((int64_t)p.t + per - 1) / per * p.chunks);
+  return ((int64_t)p.t + per - 1) / per * p.chunks;
 }
 
 template <int DT>
 hipError_t dispatch(MoveArgs p, hipStream_t s) {
-  const dim3 grid(move_grid<DT>(p)), wg(256);
+  const int64_t groups = move_grid<DT>(p);
+  if (groups > kMaxGroups) return hipErrorInvalidConfiguration;
+  const dim3 grid((unsigned)groups), wg(256);
   if (streams<DT>(p.slots, p.h)) hipLaunchKernelGGL((k_dispatch_rows<DT, true>), grid, wg, 0, s, p);
   else hipLaunchKernelGGL((k_dispatch_rows<DT, false>), grid, wg, 0, s, p);
   return hipGetLastError();
@@ -405,7 +407,9 @@ hipError_t dispatch(MoveArgs p, hipStream_t s) {
 
 template <int DT, bool WEIGHTED>
 hipError_t combine_as(MoveArgs p, hipStream_t s) {
-  const dim3 grid(move_grid<DT>(p)), wg(256);
+  const int64_t groups = move_grid<DT>(p);
+  if (groups > kMaxGroups) return hipErrorInvalidConfiguration;
+  const dim3 grid((unsigned)groups), wg(256);
   if (streams<DT>(p.t, p.h)) hipLaunchKernelGGL((k_combine_rows<DT, WEIGHTED, true>), grid, wg, 0, s, p);
   else hipLaunchKernelGGL((k_combine_rows<DT, WEIGHTED, false>), grid, wg, 0, s, p);
   return hipGetLastError();
@@ -418,7 +422,9 @@ hipError_t combine(const MoveArgs& p, hipStream_t s) {
 
 template <int DT, int LANES>
 hipError_t combine_grad_as(const GradArgs& p, hipStream_t s) {
-  const dim3 grid((unsigned)((p.t + 256 / LANES - 1) / (256 / LANES))), wg(256);
+  const int groups = (p.t + 256 / LANES - 1) / (256 / LANES);
+  if (groups > kMaxGroups) return hipErrorInvalidConfiguration;
+  const dim3 grid((unsigned)groups), wg(256);
   if (streams<DT>(p.slots, p.h)) hipLaunchKernelGGL((k_combine_rows_grad<DT, LANES, true>), grid, wg, 0, s, p);
   else hipLaunchKernelGGL((k_combine_rows_grad<DT, LANES, false>), grid, wg, 0, s, p);
   return hipGetLastError();

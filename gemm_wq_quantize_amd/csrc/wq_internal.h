@@ -178,6 +178,10 @@ hipError_t launch_gemv_ternary_sb(const uint8_t* w, const uint8_t* codebook, con
 // Rows sorted by bin and moved there and back (route_rows.hip).
 constexpr int kMaxBins = 1024;                 // per-wave counters of a sort fit LDS
 constexpr int64_t kMaxSlots = int64_t(1) << 24;  // t * topk
+// Workgroups of 256 lanes in a launch (HIP counts its lanes in 32 bits).  The
+// launches below that would need more return hipErrorInvalidConfiguration
+// before anything is enqueued.
+constexpr int64_t kMaxGroups = ((int64_t(1) << 32) - 1) / 256;
 // Upper bound of the tiles of 2^shift rows that `rows` sorted rows in `bins`
 // bins make: every bin adds at most one partial tile.
 inline int64_t row_tiles_bound(int64_t rows, int64_t bins, int shift) {

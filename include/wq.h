@@ -385,8 +385,8 @@ int wq_sort_rows(const int32_t* ids, int64_t t, int64_t topk, int64_t bins, int3
  *         are left as they were.
  * Its gradient with respect to x is wq_combine_rows of out's gradient with
  * weights NULL.  Requires t * topk <= 2^24, h < 2^31, x and out aligned to
- * the element (rows of any length; 16-byte aligned ones are fastest), at most
- * 2^31 - 1 workgroups of 1024 elements.
+ * the element (rows of any length; 16-byte aligned ones are fastest), and no
+ * more than 2^24 - 1 pieces of 4 KiB in all rows of x (WQ_ESHAPE beyond).
  */
 int wq_dispatch_rows(const void* x, int dtype, const int32_t* place, int64_t t, int64_t topk, int64_t h, void* out,
                      void* stream);
@@ -438,7 +438,8 @@ int wq_combine_rows_grad(const void* d_out, const void* rows, int dtype, const i
  * bf16((q - z) * s) as in wq_gemm_w4a16, except with one scale per column and
  * a zero_const that is a multiple of 1/8 within 16 (then q - z is exact).
  * Bitwise repeatable.  Requires k % 64 == 0, k <= 2^22, slots <= 2^24,
- * 1 <= experts <= 1024, n * experts < 2^31, a gathered `a` below 2 GiB;
+ * 1 <= experts <= 1024, n * experts < 2^31, no more than 2^24 - 1 workgroups
+ * (16 or 128 rows by 16 to 256 columns each), a gathered `a` below 2 GiB;
  * a, b and c_out 16-byte aligned, scales and zeros 4-byte (whole aligned
  * 4-byte words are read, so the 2 bytes after the last element may be read
  * and are ignored).
@@ -472,8 +473,9 @@ int64_t wq_lora_workspace(int64_t t, int64_t k, int64_t adapters, int64_t rank);
  * scales are assumed for rows that have an adapter; those without are copied
  * bit for bit.  Bitwise repeatable.
  * Requires k % 32 == 0, rank a multiple of 8 up to 128, 1 <= adapters <= 1024,
- * t <= 2^24, n < 2^31, k <= 2^24; x, a, b and workspace 16-byte aligned, base
- * and out to the element.
+ * t <= 2^24, n < 2^31, k <= 2^24, no more than 2^24 - 1 workgroups (16 or 32
+ * rows by up to 1024 columns each); x, a, b and workspace 16-byte aligned,
+ * base and out to the element.
  */
 int wq_lora(const uint16_t* x, int64_t t, int64_t k, const int32_t* order, const int32_t* offsets, int64_t adapters,
             const uint16_t* a, const uint16_t* b, int64_t rank, const float* scales, const void* base, void* out,

@@ -157,3 +157,25 @@ def test_lora_binding_refusals():
                       (dict(order=z(4, torch.int64)), "int32")):
         with pytest.raises(ValueError, match=match):
             g.wq_lora(**{**args, **kw})
+
+
+def test_more_workgroups_than_a_launch_holds(lib):
+    """2^32 lanes and more: refused before anything is enqueued."""
+    d = lambda t, h, dt=2: lib.wq_dispatch_rows(FAKE, dt, FAKE, t, 1, h, FAKE, None)
+    c = lambda t, h, dt=2, w=FAKE: lib.wq_combine_rows(FAKE, dt, FAKE, w, t, 1, h, FAKE, None)
+    for f in (d, c):
+        assert f(1 << 20, 32768) == g.WQ_ESHAPE            # 2^24 pieces of 4 KiB
+        assert f(1 << 24, 1025) == g.WQ_ESHAPE             # a workgroup a row
+        assert f(1 << 24, 2048, dt=1) == g.WQ_ESHAPE
+        assert f(1 << 20, 16384, dt=0) == g.WQ_ESHAPE
+    assert c(1 << 20, 32768, w=None) == g.WQ_ESHAPE
+    for dt, h in ((2, 1025), (1, 4096), (0, 513)):
+        assert lib.wq_combine_rows_grad(FAKE, FAKE, dt, FAKE, FAKE, 1 << 24, 1, h, FAKE, FAKE, None) == g.WQ_ESHAPE
+    e = lambda slots, experts, n: lib.wq_gemm_w4a16_experts(FAKE, slots, None, 1, FAKE, slots, experts, FAKE, 1, FAKE,
+                                                            None, 64, 8.0, n, 64, FAKE, None)
+    assert e(1024, 1024, (1 << 21) - 1) == g.WQ_ESHAPE     # 1024 row tiles x 2^15 of 64 columns
+    assert e(1 << 24, 1, 40000) == g.WQ_ESHAPE             # 2^17 row tiles x 157 of 256 columns
+    lo = lambda t, adapters, n: lib.wq_lora(FAKE, t, 64, FAKE, FAKE, adapters, FAKE, FAKE, 16, FAKE, FAKE, FAKE, 2, n,
+                                            FAKE, 1 << 40, None)
+    assert lo(1 << 24, 1, 1 << 15) == g.WQ_ESHAPE          # (2^19 + 2) row tiles x 32 of 1024 columns
+    assert lo(1 << 10, 1024, 1 << 25) == g.WQ_ESHAPE       # 1024 row tiles x 2^15 of 1024 columns
